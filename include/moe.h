@@ -460,6 +460,80 @@ int moe_forward_noalloc(const moe_problem_t* p, const void* x, const int32_t* to
  * MOE_ERR_CUDA.  No counterpart on the pages.  Allocates nothing. */
 int moe_forward_noalloc_status(void* stream);
 
+/* ---- token permutation and its gradients --------------------------------------
+ * Source: the "Current PyTorch path" of "factor_moe_fused_gemm.cu": the gather
+ * of the routed rows and the index_add of the weighted ones, as operators of
+ * their own for a caller with its own expert computation, and in training.
+ * i = t*K + k; inv_perm (T*K) and sorted_ids (cap) as moe_align writes them; a
+ * negative inv_perm entry is another shard's assignment.  Rows have H elements
+ * of `dtype`; any H >= 1 and any alignment of the element type (16-byte rows
+ * and buffers move 16 bytes at a time).  T == 0 does nothing.  Results do not
+ * depend on the schedule.  Skipped when *dev_status != 0 (it may be NULL).
+ *
+ * moe_permute_tokens: x_sorted[inv_perm[i]] = x[i / K]; rows of padding slots
+ * (sorted_ids[s] >= T*K) are set to zero, so x_sorted (cap, H) is written
+ * whole.  dtype MOE_F32, MOE_BF16 or MOE_E4M3 (rows of codes).
+ * moe_permute_tokens_backward: grad_x[t] = sum_k grad_sorted[inv_perm[t*K+k]]
+ * in k order, fp32, rounded once.  Padding rows are not read.
+ * moe_unpermute_tokens: out[t] = sum_k topk_weights[t, k] * y[inv_perm[t*K+k]],
+ * fp32 in k order, rounded once; y (cap, H), out (T, H), padding rows of y are
+ * not read.
+ * moe_unpermute_tokens_backward: grad_y[inv_perm[i]] = topk_weights[i] *
+ * grad_out[i / K] rounded once, padding rows zero; grad_weights[i] =
+ * grad_out[i / K] . y[inv_perm[i]] in fp32, 0 for another shard's assignment.
+ * The last three take MOE_F32 or MOE_BF16; topk_weights (T, K) fp32. */
+int moe_permute_tokens(const void* x, int dtype, int T, int H, int K, const int32_t* inv_perm,
+                       const int32_t* sorted_ids, size_t cap, void* x_sorted,
+                       int32_t* dev_status, void* stream);
+int moe_permute_tokens_backward(const void* grad_sorted, int dtype, int T, int H, int K,
+                                const int32_t* inv_perm, size_t cap, void* grad_x,
+                                int32_t* dev_status, void* stream);
+int moe_unpermute_tokens(const void* y, int dtype, int T, int H, int K, const float* topk_weights,
+                         const int32_t* inv_perm, size_t cap, void* out, int32_t* dev_status,
+                         void* stream);
+int moe_unpermute_tokens_backward(const void* grad_out, const void* y, int dtype, int T, int H,
+                                  int K, const float* topk_weights, const int32_t* inv_perm,
+                                  const int32_t* sorted_ids, size_t cap, void* grad_y,
+                                  float* grad_weights, int32_t* dev_status, void* stream);
+
+/* ---- e4m3 codes with a scale per 128 columns ----------------------------------
+ * The operand format of DeepSeek-V3's fp8 layers.  No counterpart on the pages
+ * (their fp8 activations have one scale per tensor).
+ * For columns [128b, 128b + 128) of a row of v (the last block may be short):
+ *   m = max(max |v|, 2^-100), scale[t, b] = m / 448,
+ *   xq = e4m3_rn_satfinite(v * (448 / m)), in fp32 with IEEE rounding.
+ * x (T, H) in x_dtype (MOE_BF16 or MOE_F32), v = x; with gated = 1, x (T, 2H)
+ * holds gate then up and v = gate / (1 + e^-gate) * up in fp32 (fast exponential
+ * and division).  xq (T, H) codes, scale (T, ceil(H/128)) fp32.  Any H >= 1.
+ * A NaN becomes a NaN code; a block with an infinity gets an infinite scale. */
+int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, uint8_t* xq,
+                           float* scale, void* stream);
+
+/* ---- products of block-scaled e4m3 operands ------------------------------------
+ * out[m, n] = sum_b a_scale[m, b] * w_scale[n / 128, b]
+ *                   * sum_{k in [128b, 128b + 128)} a[m, k] * w[n, k]
+ * in fp32, rounded once to out_dtype (MOE_BF16 or MOE_F32).
+ *   a (M, K) codes, a_scale (M, ceil(K/128)) fp32 as moe_quantize_fp8_block
+ *   writes them; w (N, K) codes, w_scale (ceil(N/128), ceil(K/128)) fp32, one
+ *   scale per 128 x 128 block (the last ones may be short); out (M, N).
+ * K must be a multiple of 16 (else MOE_ERR_UNSUPPORTED); any N >= 1; M == 0
+ * does nothing.  a and w 16-byte aligned.  The gradient with respect to a is the
+ * same product with the transposed codes and the transposed block scales.
+ *
+ * moe_grouped_gemm_fp8_block: row s of an align block with expert e times w[e]:
+ *   a (cap, K) and a_scale (cap, ceil(K/128)) in sorted order, w (E, N, K),
+ *   w_scale (E, ceil(N/128), ceil(K/128)), block_info / num_blocks from
+ *   moe_align with block_m and E experts (or a shard's local ones); out (cap,
+ *   N), rows of padding slots not written.  Source: "factor_moe_fused_gemm.cu",
+ *   the per-expert products of the "Current PyTorch path". */
+int moe_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                       const float* w_scale, int M, int N, int K, void* out, int out_dtype,
+                       int32_t* dev_status, void* stream);
+int moe_grouped_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                               const float* w_scale, int E, int N, int K, size_t cap, int block_m,
+                               const int32_t* block_info, const int32_t* num_blocks, void* out,
+                               int out_dtype, int32_t* dev_status, void* stream);
+
 /* ---- test of the kernels' failure path (not for use in a model) -----------
  * Runs moe_gemm1_silu (gemm = 1) or moe_gemm2_weighted (gemm = 2) with the
  * same arguments (a_rows: x rows / hq codes for gemm 1, h for gemm 2; w and

@@ -20,6 +20,10 @@ from ._abi import (MOE_ACT_SILU, MOE_ACT_SWIGLU_CLAMP, MOE_BF16, MOE_E2M1_MX, MO
                    moe_gemm2_weighted, moe_get_device_status, moe_mx_packed_bytes,
                    moe_pack_mx_weights, moe_quantize_gather_x_fp8, moe_quantize_x_fp8,
                    moe_resolve_block_m, moe_workspace_offsets, moe_workspace_size)
+from .fp8_block import (forward_fp8_block, gemm_fp8_block, grouped_gemm_fp8_block,
+                        quantize_fp8_block)
+from .permute import (permute_tokens, permute_tokens_backward, unpermute_tokens,
+                      unpermute_tokens_backward)
 
 __all__ = ["MOE_ACT_SILU", "MOE_ACT_SWIGLU_CLAMP", "MoEError", "Problem", "make_problem", "dtype_code", "align", "Workspace", "forward",
            "pack_mx", "moe_forward_noalloc", "moe_forward_noalloc_status", "moe_mx_packed_bytes", "moe_pack_mx_weights",
@@ -31,7 +35,10 @@ __all__ = ["MOE_ACT_SILU", "MOE_ACT_SWIGLU_CLAMP", "MoEError", "Problem", "make_
            "moe_gemm1_silu", "moe_gemm1_silu_gather",
            "moe_gemm2_default_splits", "moe_gemm2_weighted",
            "moe_get_device_status", "moe_quantize_x_fp8", "moe_resolve_block_m",
-           "moe_workspace_offsets", "moe_workspace_size"]
+           "moe_workspace_offsets", "moe_workspace_size",
+           "permute_tokens", "permute_tokens_backward", "unpermute_tokens",
+           "unpermute_tokens_backward", "quantize_fp8_block", "gemm_fp8_block",
+           "grouped_gemm_fp8_block", "forward_fp8_block"]
 
 
 def dtype_code(dt) -> int:

@@ -39,7 +39,9 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_resolve_block_m", "moe_a
            "moe_pack_mx_weights", "moe_quantize_gather_x_fp8", "moe_device_info",
            "moe_gather_rows", "moe_align_local", "moe_route_align", "moe_align_scratch_bytes",
            "moe_combine_finish", "moe_forward_noalloc_status", "moe_test_gemm_wait_timeout",
-           "moe_gemm1_silu_gather")
+           "moe_gemm1_silu_gather", "moe_permute_tokens", "moe_permute_tokens_backward",
+           "moe_unpermute_tokens", "moe_unpermute_tokens_backward", "moe_quantize_fp8_block",
+           "moe_gemm_fp8_block", "moe_grouped_gemm_fp8_block")
 
 MOE_STATIC_SCRATCH_BYTES = 64 << 20
 MOE_ACT_SILU, MOE_ACT_SWIGLU_CLAMP = 0, 1
@@ -151,6 +153,22 @@ def _declare(L):
     L.moe_forward_noalloc_status.argtypes = [vp]
     L.moe_get_device_status.restype = i32
     L.moe_get_device_status.argtypes = [vp, vp]
+    L.moe_permute_tokens.restype = i32
+    L.moe_permute_tokens.argtypes = [vp, i32, i32, i32, i32, vp, vp, sz, vp, vp, vp]
+    L.moe_permute_tokens_backward.restype = i32
+    L.moe_permute_tokens_backward.argtypes = [vp, i32, i32, i32, i32, vp, sz, vp, vp, vp]
+    L.moe_unpermute_tokens.restype = i32
+    L.moe_unpermute_tokens.argtypes = [vp, i32, i32, i32, i32, vp, vp, sz, vp, vp, vp]
+    L.moe_unpermute_tokens_backward.restype = i32
+    L.moe_unpermute_tokens_backward.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, sz,
+                                                vp, vp, vp, vp]
+    L.moe_quantize_fp8_block.restype = i32
+    L.moe_quantize_fp8_block.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+    L.moe_gemm_fp8_block.restype = i32
+    L.moe_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    L.moe_grouped_gemm_fp8_block.restype = i32
+    L.moe_grouped_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, i32, i32, sz, i32, vp, vp, vp,
+                                             i32, vp, vp]
     L.moe_device_info.restype = i32
     L.moe_device_info.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.moe_mx_packed_bytes.restype = sz
@@ -345,6 +363,56 @@ def moe_forward_noalloc_status(stream=None) -> int:
     if rc == MOE_ERR_CUDA:
         raise MoEError(rc, "moe_forward_noalloc_status")
     return rc
+
+
+def moe_permute_tokens(x, dtype, T, H, K, inv_perm, sorted_ids, cap, x_sorted, dev_status=None,
+                       stream=None):
+    _check(lib().moe_permute_tokens(_p(x), dtype, T, H, K, _p(inv_perm), _p(sorted_ids), cap,
+                                    _p(x_sorted), _p(dev_status), _stream(stream)),
+           "moe_permute_tokens")
+
+
+def moe_permute_tokens_backward(grad_sorted, dtype, T, H, K, inv_perm, cap, grad_x,
+                                dev_status=None, stream=None):
+    _check(lib().moe_permute_tokens_backward(_p(grad_sorted), dtype, T, H, K, _p(inv_perm), cap,
+                                             _p(grad_x), _p(dev_status), _stream(stream)),
+           "moe_permute_tokens_backward")
+
+
+def moe_unpermute_tokens(y, dtype, T, H, K, topk_weights, inv_perm, cap, out, dev_status=None,
+                         stream=None):
+    _check(lib().moe_unpermute_tokens(_p(y), dtype, T, H, K, _p(topk_weights), _p(inv_perm), cap,
+                                      _p(out), _p(dev_status), _stream(stream)),
+           "moe_unpermute_tokens")
+
+
+def moe_unpermute_tokens_backward(grad_out, y, dtype, T, H, K, topk_weights, inv_perm, sorted_ids,
+                                  cap, grad_y, grad_weights, dev_status=None, stream=None):
+    _check(lib().moe_unpermute_tokens_backward(_p(grad_out), _p(y), dtype, T, H, K,
+                                               _p(topk_weights), _p(inv_perm), _p(sorted_ids),
+                                               cap, _p(grad_y), _p(grad_weights),
+                                               _p(dev_status), _stream(stream)),
+           "moe_unpermute_tokens_backward")
+
+
+def moe_quantize_fp8_block(x, x_dtype, T, H, gated, xq, scale, stream=None):
+    _check(lib().moe_quantize_fp8_block(_p(x), x_dtype, T, H, int(gated), _p(xq), _p(scale),
+                                        _stream(stream)), "moe_quantize_fp8_block")
+
+
+def moe_gemm_fp8_block(a, a_scale, w, w_scale, M, N, K, out, out_dtype, dev_status=None,
+                       stream=None):
+    _check(lib().moe_gemm_fp8_block(_p(a), _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out),
+                                    out_dtype, _p(dev_status), _stream(stream)),
+           "moe_gemm_fp8_block")
+
+
+def moe_grouped_gemm_fp8_block(a, a_scale, w, w_scale, E, N, K, cap, block_m, block_info,
+                               num_blocks, out, out_dtype, dev_status=None, stream=None):
+    _check(lib().moe_grouped_gemm_fp8_block(_p(a), _p(a_scale), _p(w), _p(w_scale), E, N, K, cap,
+                                            block_m, _p(block_info), _p(num_blocks), _p(out),
+                                            out_dtype, _p(dev_status), _stream(stream)),
+           "moe_grouped_gemm_fp8_block")
 
 
 def moe_mx_packed_bytes(E, R, K, sections):

@@ -208,6 +208,56 @@ cudaError_t launch_quantize_gather_x(const void* x, int x_dtype, int T, int H, i
 cudaError_t launch_combine_finish(const float* acc, int T, int H, int out_dtype, void* out,
                                   const int32_t* status, cudaStream_t s);
 
+// Token rows to the sorted list and back, and their gradients (permute.cu).
+// row_bytes: bytes of a row of x; weights null: all one; cap: rows of the
+// sorted buffer and entries of sorted_ids.
+cudaError_t launch_permute(const void* x, int T, long long row_bytes, int K,
+                           const int32_t* inv_perm, const int32_t* sorted_ids, long long cap,
+                           void* xs, const int32_t* status, cudaStream_t s);
+cudaError_t launch_unpermute(const void* y, int dtype, const float* weights, int T, int K, int H,
+                             const int32_t* inv_perm, long long cap, void* out,
+                             const int32_t* status, cudaStream_t s);
+cudaError_t launch_unpermute_backward(const void* dout, const void* y, int dtype,
+                                      const float* weights, int T, int K, int H,
+                                      const int32_t* inv_perm, const int32_t* sorted_ids,
+                                      long long cap, void* dy, float* dw, const int32_t* status,
+                                      cudaStream_t s);
+// e4m3 codes with a scale per 128 columns (quant_block.cu).  gated: x rows
+// hold 2H columns, gate then up.
+cudaError_t launch_quantize_block(const void* x, int x_dtype, int T, int H, int gated,
+                                  uint8_t* xq, float* scale, cudaStream_t s);
+
+// Arguments of a product of block-scaled e4m3 operands (gemm_fp8b.cu).
+struct Fp8bArgs {
+  int M;                       // rows of the plain product
+  int N, K;
+  int E;                       // weight matrices (1 for the plain product)
+  int n_tiles, k_tiles, band;  // k_tiles: blocks of 128 along K
+  int n_scales;                // scale rows per weight matrix, ceil(N / 128)
+  const float* a_scale;        // (rows, k_tiles)
+  const float* w_scale;        // (E, n_scales, k_tiles)
+  const int32_t* block_info;   // align's row blocks, or null: M rows in order
+  const int32_t* num_blocks;
+  int max_blocks;              // entries of block_info, or ceil(M / 128)
+  int subs;                    // 128-row parts of an align block
+  long long cap;               // rows of a
+  void* out;                   // (rows, N)
+  int out_bf16, wide_out;      // wide_out: 16-byte stores fit every row
+  int32_t* status;
+  unsigned long long timeout_ns;
+  int starve;                  // failure-path test: the producer issues no copies
+};
+// tmA / tmAShort: a, boxes of 128 x 128 and 32 x 128 (rows x bytes); tmB: the
+// E * N weight rows, box of 256 x 128.
+cudaError_t launch_fp8b_gemm(Fp8bArgs a, const CUtensorMap& tmA, const CUtensorMap& tmAShort,
+                             const CUtensorMap& tmB, int sms, cudaStream_t s);
+
+// Host helpers of moe_abi.cu: the current device's SM count, and the tensor
+// map of a row-major byte tensor (16-byte aligned, inner a multiple of 16)
+// read in 128-byte swizzled boxes.
+int device_sm_count();
+int make_byte_map(CUtensorMap* tm, const void* base, long long inner, long long outer,
+                  int box_inner, int box_outer);
 // Align blocks of 256 rows: the largest token tile of the bf16/fp32 GEMMs.
 constexpr int kPairBlockM = 256;
 

@@ -570,6 +570,24 @@ int run_gemm2_mx(const moe_problem_t* p, const void* hq, const void* w2, const u
 
 }  // namespace
 
+int moe::device_sm_count() { return sm_count(); }
+
+int moe::make_byte_map(CUtensorMap* tm, const void* base, long long inner, long long outer,
+                       int box_inner, int box_outer) {
+  auto enc = encoder();
+  if (enc == nullptr) return MOE_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner),
+                             static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
 int moe::validate_forward_problem(const moe_problem_t* p) {
   const int rc = check_problem(p);
   return rc != MOE_OK ? rc : check_gemm_shapes(p);

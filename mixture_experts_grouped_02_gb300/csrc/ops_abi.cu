@@ -1,0 +1,181 @@
+// ops_abi.cu -- C entry points of the token permutation, the 128-column fp8
+// quantiser and the block-scaled products: argument checks and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "internal.h"
+
+using namespace moe;
+
+namespace {
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+// Element bytes of `dtype`, 0 when it is not one of the two row types (or,
+// with `codes`, of the three).
+int elem_bytes(int dtype, bool codes = false) {
+  if (dtype == MOE_F32) return 4;
+  if (dtype == MOE_BF16) return 2;
+  return codes && dtype == MOE_E4M3 ? 1 : 0;
+}
+
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// Sizes shared by the four permutation entry points; cap is an int32 slot
+// count in the lists.
+int check_list(int T, int H, int K, size_t cap, int es) {
+  if (T < 0 || H <= 0 || K <= 0 || es == 0) return MOE_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * K >= (1ll << 30) || cap > 0x7fffffffull)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_gemm(int E, int N, int K, int out_dtype) {
+  if (E <= 0 || N <= 0 || K <= 0 || elem_bytes(out_dtype) == 0) return MOE_ERR_INVALID_ARG;
+  // TMA rows start on 16 bytes, and row coordinates are 32-bit
+  if (K % 16 != 0 || static_cast<long long>(E) * N >= (1ll << 31) - 256)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int out_dtype,
+             cudaStream_t s) {
+  const int es = elem_bytes(out_dtype);
+  if (!x || !a.a_scale || !w || !a.w_scale || !a.out || !aligned(x, 16) || !aligned(w, 16) ||
+      !aligned(a.a_scale, 4) || !aligned(a.w_scale, 4) || !aligned(a.out, es))
+    return MOE_ERR_INVALID_ARG;
+  a.k_tiles = (a.K + 127) / 128;
+  a.n_scales = (a.N + 127) / 128;
+  a.cap = rows;
+  a.out_bf16 = out_dtype == MOE_BF16;
+  a.wide_out = (static_cast<long long>(a.N) * es) % 16 == 0 && aligned(a.out, 16);
+  a.timeout_ns = kWaitTimeoutNs;
+  CUtensorMap tmA, tmAShort, tmB;
+  int rc = make_byte_map(&tmA, x, a.K, rows, 128, 128);
+  if (rc == MOE_OK) rc = make_byte_map(&tmAShort, x, a.K, rows, 128, 32);
+  if (rc == MOE_OK) rc = make_byte_map(&tmB, w, a.K, static_cast<long long>(a.E) * a.N, 128, 256);
+  if (rc != MOE_OK) return rc;
+  return cuda_status(launch_fp8b_gemm(a, tmA, tmAShort, tmB, device_sm_count(), s));
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_permute_tokens(const void* x, int dtype, int T, int H, int K, const int32_t* inv_perm,
+                       const int32_t* sorted_ids, size_t cap, void* x_sorted,
+                       int32_t* dev_status, void* stream) {
+  const int es = elem_bytes(dtype, true);
+  const int rc = check_list(T, H, K, cap, es);
+  if (rc != MOE_OK || T == 0) return rc;
+  if (!x || !inv_perm || !sorted_ids || !x_sorted || !aligned(x, es) || !aligned(x_sorted, es))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_permute(x, T, static_cast<long long>(H) * es, K, inv_perm, sorted_ids,
+                                    static_cast<long long>(cap), x_sorted, dev_status,
+                                    as_stream(stream)));
+}
+
+int moe_permute_tokens_backward(const void* grad_sorted, int dtype, int T, int H, int K,
+                                const int32_t* inv_perm, size_t cap, void* grad_x,
+                                int32_t* dev_status, void* stream) {
+  const int es = elem_bytes(dtype);
+  const int rc = check_list(T, H, K, cap, es);
+  if (rc != MOE_OK || T == 0) return rc;
+  if (!grad_sorted || !inv_perm || !grad_x || !aligned(grad_sorted, es) || !aligned(grad_x, es))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_unpermute(grad_sorted, dtype, nullptr, T, K, H, inv_perm,
+                                      static_cast<long long>(cap), grad_x, dev_status,
+                                      as_stream(stream)));
+}
+
+int moe_unpermute_tokens(const void* y, int dtype, int T, int H, int K, const float* topk_weights,
+                         const int32_t* inv_perm, size_t cap, void* out, int32_t* dev_status,
+                         void* stream) {
+  const int es = elem_bytes(dtype);
+  const int rc = check_list(T, H, K, cap, es);
+  if (rc != MOE_OK || T == 0) return rc;
+  if (!y || !topk_weights || !inv_perm || !out || !aligned(y, es) || !aligned(out, es))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_unpermute(y, dtype, topk_weights, T, K, H, inv_perm,
+                                      static_cast<long long>(cap), out, dev_status,
+                                      as_stream(stream)));
+}
+
+int moe_unpermute_tokens_backward(const void* grad_out, const void* y, int dtype, int T, int H,
+                                  int K, const float* topk_weights, const int32_t* inv_perm,
+                                  const int32_t* sorted_ids, size_t cap, void* grad_y,
+                                  float* grad_weights, int32_t* dev_status, void* stream) {
+  const int es = elem_bytes(dtype);
+  const int rc = check_list(T, H, K, cap, es);
+  if (rc != MOE_OK || T == 0) return rc;
+  if (!grad_out || !y || !topk_weights || !inv_perm || !sorted_ids || !grad_y || !grad_weights ||
+      !aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_y, es))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_unpermute_backward(
+      grad_out, y, dtype, topk_weights, T, K, H, inv_perm, sorted_ids,
+      static_cast<long long>(cap), grad_y, grad_weights, dev_status, as_stream(stream)));
+}
+
+int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, uint8_t* xq,
+                           float* scale, void* stream) {
+  const int es = elem_bytes(x_dtype);
+  if (T < 0 || H <= 0 || es == 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !xq || !scale || !aligned(x, es)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(
+      launch_quantize_block(x, x_dtype, T, H, gated, xq, scale, as_stream(stream)));
+}
+
+int moe_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                       const float* w_scale, int M, int N, int K, void* out, int out_dtype,
+                       int32_t* dev_status, void* stream) {
+  const int rc = check_gemm(1, N, K, out_dtype);
+  if (rc != MOE_OK || M < 0) return rc != MOE_OK ? rc : MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  Fp8bArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.E = 1;
+  g.max_blocks = M / 128 + (M % 128 != 0);
+  g.subs = 1;
+  g.a_scale = a_scale;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.status = dev_status;
+  return run_gemm(g, a, M, w, out_dtype, as_stream(stream));
+}
+
+int moe_grouped_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                               const float* w_scale, int E, int N, int K, size_t cap, int block_m,
+                               const int32_t* block_info, const int32_t* num_blocks, void* out,
+                               int out_dtype, int32_t* dev_status, void* stream) {
+  const int rc = check_gemm(E, N, K, out_dtype);
+  if (rc != MOE_OK) return rc;
+  if (block_m != 16 && block_m != 32 && block_m != 64 && block_m != 128 && block_m != 256)
+    return MOE_ERR_INVALID_ARG;
+  if (cap > 0x7fffffffull - 256) return MOE_ERR_UNSUPPORTED;
+  if (cap / block_m == 0) return MOE_OK;
+  if (!block_info || !num_blocks || !aligned(block_info, 16)) return MOE_ERR_INVALID_ARG;
+  Fp8bArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.N = N;
+  g.K = K;
+  g.E = E;
+  g.block_info = block_info;
+  g.num_blocks = num_blocks;
+  g.max_blocks = static_cast<int>(cap / block_m);
+  g.subs = block_m > 128 ? block_m / 128 : 1;
+  g.a_scale = a_scale;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.status = dev_status;
+  return run_gemm(g, a, static_cast<long long>(cap), w, out_dtype, as_stream(stream));
+}
+
+}  // extern "C"

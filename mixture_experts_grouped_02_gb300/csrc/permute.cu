@@ -1,0 +1,326 @@
+// permute.cu -- token rows to the expert-sorted list and back, with their
+// gradients.
+//
+// With i = t*K + k the flat index of token t's k-th choice, slot(i) =
+// inv_perm[i] its place in the padded list moe_align makes and sorted_ids its
+// inverse:
+//   permute             xs[slot(i)] = x[i / K], rows of padding slots zero
+//   its gradient        dx[t] = sum_k dxs[slot(tK + k)]
+//   unpermute           out[t] = sum_k w[t, k] * y[slot(tK + k)]
+//   its gradients       dy[slot(i)] = w[i] * dout[i / K], padding rows zero
+//                       dw[i] = dout[i / K] . y[slot(i)]
+// Sums run in fp32 in k order (dw: lane partial sums and a fixed tree) and are
+// rounded once to the rows' type, so results do not depend on the schedule.
+// An assignment to another shard's expert (slot < 0) adds nothing and gets
+// dw = 0.  Sources: the "Current PyTorch path" of "factor_moe_fused_gemm.cu"
+// (gather of the routed rows, index_add of the weighted ones), whose autograd
+// these gradients are.
+//
+// All four move bytes and compute next to nothing: HBM bounds them, and the
+// launch bounds the smallest.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "bounds.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Slots a warp looks at for padding rows.  Padding comes in runs (an expert's
+// last block, the tail of the list), so small pieces spread it over the SMs.
+constexpr int kPadSlots = 8;
+
+// A run of V elements of type T, loaded and stored as one word.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+  using type = uint4;
+};
+template <>
+struct Word<4> {
+  using type = uint32_t;
+};
+template <>
+struct Word<2> {
+  using type = uint16_t;
+};
+template <>
+struct Word<1> {
+  using type = uint8_t;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const typename Word<sizeof(T) * V>::type& w, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = static_cast<float>(*reinterpret_cast<const T*>(&w));
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(p[i] << 16);
+      f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+    }
+  } else {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+}
+
+// One rounding to nearest even from fp32 to the rows' type.
+template <typename T, int V>
+__device__ __forceinline__ typename Word<sizeof(T) * V>::type pack(const float (&f)[V]) {
+  if constexpr (V == 1) {
+    const T v = static_cast<T>(f[0]);
+    return *reinterpret_cast<const typename Word<sizeof(T)>::type*>(&v);
+  } else if constexpr (sizeof(T) == 2) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(p[0], p[1], p[2], p[3]);
+  } else {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+}
+
+// Zero rows of the padding slots among the kPadSlots slots of job `job`, by
+// one warp.
+template <typename W>
+__device__ __forceinline__ void zero_padding(const int32_t* __restrict__ sorted_ids, long long job,
+                                             long long cap, int n_assign, int row_words,
+                                             W* __restrict__ rows, int lane) {
+  const long long s0 = job * kPadSlots;
+  const bool pad = lane < kPadSlots && s0 + lane < cap && sorted_ids[s0 + lane] >= n_assign;
+  unsigned todo = __ballot_sync(0xffffffffu, pad);
+  while (todo != 0) {
+    const int u = __ffs(todo) - 1;
+    todo &= todo - 1;
+    W* row = rows + (s0 + u) * row_words;
+    for (int c = lane; c < row_words; c += 32) row[c] = W{};
+  }
+}
+
+// Jobs [0, T * chunks): 256 words of a token's row, read once and written to
+// the slots of its K choices.  Jobs after them: padding rows.
+template <typename W>
+__global__ void __launch_bounds__(kThreads)
+    permute_kernel(const W* __restrict__ x, int T, int K, int row_words, int chunks,
+                   const int32_t* __restrict__ inv_perm, const int32_t* __restrict__ sorted_ids,
+                   long long cap, W* __restrict__ xs, const int32_t* status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  if (status != nullptr && *status != 0) return;
+  const long long token_jobs = static_cast<long long>(T) * chunks;
+  if (blockIdx.x >= token_jobs) {
+    const int warp = threadIdx.x >> 5;
+    zero_padding(sorted_ids, (blockIdx.x - token_jobs) * kWarps + warp, cap, T * K, row_words, xs,
+                 threadIdx.x & 31);
+    return;
+  }
+  const int t = static_cast<int>(blockIdx.x / chunks);
+  const int c = static_cast<int>(blockIdx.x - static_cast<long long>(t) * chunks) * kThreads +
+                threadIdx.x;
+  if (c >= row_words) return;
+  const W v = x[static_cast<long long>(t) * row_words + c];
+  for (int k = 0; k < K; ++k) {
+    const long long slot = inv_perm[static_cast<long long>(t) * K + k];
+    if (slot >= 0 && in_bounds(slot < cap, status)) xs[slot * row_words + c] = v;
+  }
+}
+
+// out[t] = sum_k w[t, k] * y[slot(tK + k)] (w null: all one).  Words of the
+// output are dealt to threads across token boundaries; `group` tokens make up
+// one grid row, which keeps the word index in 32 bits.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+    unpermute_kernel(const T* __restrict__ y_, const float* __restrict__ weights, int tokens,
+                     int K, int row_words, int group, const int32_t* __restrict__ inv_perm,
+                     long long cap, T* __restrict__ out_, const int32_t* status) {
+  using W = typename Word<sizeof(T) * V>::type;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (status != nullptr && *status != 0) return;
+  const W* y = reinterpret_cast<const W*>(y_);
+  W* out = reinterpret_cast<W*>(out_);
+  const int idx = blockIdx.x * kThreads + threadIdx.x;
+  const int tl = idx / row_words;
+  const int c = idx - tl * row_words;
+  for (long long g = blockIdx.y; g * group < tokens; g += gridDim.y) {
+    const long long t = g * group + tl;
+    if (tl >= group || t >= tokens) continue;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int k = 0; k < K; ++k) {
+      const long long slot = inv_perm[t * K + k];
+      if (slot < 0 || !in_bounds(slot < cap, status)) continue;
+      const float w = weights != nullptr ? weights[t * K + k] : 1.0f;
+      float f[V];
+      unpack<T, V>(y[slot * row_words + c], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+    }
+    out[t * row_words + c] = pack<T, V>(acc);
+  }
+}
+
+// A warp per assignment: its dy row and its dw; then padding rows.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+    unpermute_backward_kernel(const T* __restrict__ dout_, const T* __restrict__ y_,
+                              const float* __restrict__ weights, int n_assign, int K,
+                              int row_words, const int32_t* __restrict__ inv_perm,
+                              const int32_t* __restrict__ sorted_ids, long long cap,
+                              T* __restrict__ dy_, float* __restrict__ dw,
+                              const int32_t* status) {
+  using W = typename Word<sizeof(T) * V>::type;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (status != nullptr && *status != 0) return;
+  const int lane = threadIdx.x & 31;
+  const long long job = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  W* dy = reinterpret_cast<W*>(dy_);
+  if (job >= n_assign) {
+    zero_padding(sorted_ids, job - n_assign, cap, n_assign, row_words, dy, lane);
+    return;
+  }
+  const long long slot = inv_perm[job];
+  if (slot < 0 || !in_bounds(slot < cap, status)) {
+    if (lane == 0) dw[job] = 0.0f;
+    return;
+  }
+  const float w = weights[job];
+  const W* g = reinterpret_cast<const W*>(dout_) + (job / K) * row_words;
+  const W* y = reinterpret_cast<const W*>(y_) + slot * row_words;
+  dy += slot * row_words;
+  float dot = 0.0f;
+  for (int c = lane; c < row_words; c += 32) {
+    float gf[V], yf[V];
+    unpack<T, V>(g[c], gf);
+    unpack<T, V>(y[c], yf);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dot = fmaf(gf[i], yf[i], dot);
+      gf[i] *= w;
+    }
+    dy[c] = pack<T, V>(gf);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+  if (lane == 0) dw[job] = dot;
+}
+
+// Largest power of two up to 16 that divides the row and every address.
+int word_bytes(long long row_bytes, const void* a, const void* b, const void* c = nullptr) {
+  const uintptr_t all = static_cast<uintptr_t>(row_bytes) | reinterpret_cast<uintptr_t>(a) |
+                        reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) | 16u;
+  return static_cast<int>(all & (~all + 1));
+}
+
+long long pad_jobs(long long cap) { return (cap + kPadSlots - 1) / kPadSlots; }
+
+template <typename W>
+cudaError_t permute_as(const void* x, int T, int K, long long row_bytes, const int32_t* inv_perm,
+                       const int32_t* sorted_ids, long long cap, void* xs, const int32_t* status,
+                       cudaStream_t s) {
+  const int row_words = static_cast<int>(row_bytes / sizeof(W));
+  const int chunks = (row_words + kThreads - 1) / kThreads;
+  const long long grid =
+      static_cast<long long>(T) * chunks + (pad_jobs(cap) + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, permute_kernel<W>, static_cast<const W*>(x), T, K, row_words,
+                            chunks, inv_perm, sorted_ids, cap, static_cast<W*>(xs), status);
+}
+
+template <typename T, int V>
+cudaError_t unpermute_as(const void* y, const float* weights, int tokens, int K, int H,
+                         const int32_t* inv_perm, long long cap, void* out, const int32_t* status,
+                         cudaStream_t s) {
+  const int row_words = H / V;
+  const int group = std::min(tokens, std::max(1, (1 << 20) / row_words));
+  const long long rows = (static_cast<long long>(tokens) + group - 1) / group;
+  const dim3 grid((group * static_cast<long long>(row_words) + kThreads - 1) / kThreads,
+                  static_cast<unsigned>(std::min(rows, 65535ll)));
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pdl_config(grid, dim3(kThreads), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, unpermute_kernel<T, V>, static_cast<const T*>(y), weights,
+                            tokens, K, row_words, group, inv_perm, cap, static_cast<T*>(out),
+                            status);
+}
+
+template <typename T, int V>
+cudaError_t unpermute_backward_as(const void* dout, const void* y, const float* weights,
+                                  int tokens, int K, int H, const int32_t* inv_perm,
+                                  const int32_t* sorted_ids, long long cap, void* dy, float* dw,
+                                  const int32_t* status, cudaStream_t s) {
+  const long long jobs = static_cast<long long>(tokens) * K + pad_jobs(cap);
+  const unsigned grid = static_cast<unsigned>((jobs + kWarps - 1) / kWarps);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(kThreads), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, unpermute_backward_kernel<T, V>, static_cast<const T*>(dout),
+                            static_cast<const T*>(y), weights, tokens * K, K, H / V, inv_perm,
+                            sorted_ids, cap, static_cast<T*>(dy), dw, status);
+}
+
+}  // namespace
+
+cudaError_t launch_permute(const void* x, int T, long long row_bytes, int K,
+                           const int32_t* inv_perm, const int32_t* sorted_ids, long long cap,
+                           void* xs, const int32_t* status, cudaStream_t s) {
+  switch (word_bytes(row_bytes, x, xs)) {
+    case 16:
+      return permute_as<uint4>(x, T, K, row_bytes, inv_perm, sorted_ids, cap, xs, status, s);
+    case 8:
+    case 4:
+      return permute_as<uint32_t>(x, T, K, row_bytes, inv_perm, sorted_ids, cap, xs, status, s);
+    case 2:
+      return permute_as<uint16_t>(x, T, K, row_bytes, inv_perm, sorted_ids, cap, xs, status, s);
+    default:
+      return permute_as<uint8_t>(x, T, K, row_bytes, inv_perm, sorted_ids, cap, xs, status, s);
+  }
+}
+
+cudaError_t launch_unpermute(const void* y, int dtype, const float* weights, int T, int K, int H,
+                             const int32_t* inv_perm, long long cap, void* out,
+                             const int32_t* status, cudaStream_t s) {
+  const bool bf16 = dtype == MOE_BF16;
+  const bool wide = word_bytes(static_cast<long long>(H) * (bf16 ? 2 : 4), y, out) == 16;
+  if (bf16)
+    return wide ? unpermute_as<__nv_bfloat16, 8>(y, weights, T, K, H, inv_perm, cap, out, status, s)
+                : unpermute_as<__nv_bfloat16, 1>(y, weights, T, K, H, inv_perm, cap, out, status, s);
+  return wide ? unpermute_as<float, 4>(y, weights, T, K, H, inv_perm, cap, out, status, s)
+              : unpermute_as<float, 1>(y, weights, T, K, H, inv_perm, cap, out, status, s);
+}
+
+cudaError_t launch_unpermute_backward(const void* dout, const void* y, int dtype,
+                                      const float* weights, int T, int K, int H,
+                                      const int32_t* inv_perm, const int32_t* sorted_ids,
+                                      long long cap, void* dy, float* dw, const int32_t* status,
+                                      cudaStream_t s) {
+  const bool bf16 = dtype == MOE_BF16;
+  const bool wide = word_bytes(static_cast<long long>(H) * (bf16 ? 2 : 4), dout, y, dy) == 16;
+  if (bf16)
+    return wide ? unpermute_backward_as<__nv_bfloat16, 8>(dout, y, weights, T, K, H, inv_perm,
+                                                          sorted_ids, cap, dy, dw, status, s)
+                : unpermute_backward_as<__nv_bfloat16, 1>(dout, y, weights, T, K, H, inv_perm,
+                                                          sorted_ids, cap, dy, dw, status, s);
+  return wide ? unpermute_backward_as<float, 4>(dout, y, weights, T, K, H, inv_perm, sorted_ids,
+                                                cap, dy, dw, status, s)
+              : unpermute_backward_as<float, 1>(dout, y, weights, T, K, H, inv_perm, sorted_ids,
+                                                cap, dy, dw, status, s);
+}
+
+}  // namespace moe

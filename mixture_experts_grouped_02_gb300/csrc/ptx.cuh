@@ -247,8 +247,9 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
   return d;
 }
 
-// Instruction descriptor for kind::f16 / kind::tf32: fp32 accumulator,
-// A and B K-major, dense.  ab_fmt: 1 = bf16 (kind::f16), 2 = tf32 (kind::tf32).
+// Instruction descriptor for kind::f16 / kind::tf32 / kind::f8f6f4: fp32
+// accumulator, A and B K-major, dense.  ab_fmt: 1 = bf16 (kind::f16), 2 = tf32
+// (kind::tf32), 0 = e4m3 (kind::f8f6f4).
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_fmt, int M, int N) {
   return (1u << 4)                                  // D format: f32
          | (ab_fmt << 7)                            // A format
@@ -302,6 +303,16 @@ __device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, 
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
       "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// D (+)= A x B^T of 8-bit floating-point operands (formats in idesc), K = 32.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
