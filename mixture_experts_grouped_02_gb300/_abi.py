@@ -76,6 +76,8 @@ def library_path() -> str:
 def lib(build_if_missing: bool = True):
     """Load libmoe_gb300.so (building it first if it is absent or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_missing and not _build.up_to_date():
@@ -196,8 +198,15 @@ def _p(t):
     return t.data_ptr()
 
 
+# (device) -> the current stream's handle: what current_stream().cuda_stream
+# gives, without building a Stream object (0.1 us instead of 2.9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

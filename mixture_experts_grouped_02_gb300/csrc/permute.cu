@@ -31,9 +31,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Slots a warp looks at for padding rows.  Padding comes in runs (an expert's
-// last block, the tail of the list), so small pieces spread it over the SMs.
-constexpr int kPadSlots = 8;
+// Slots a CTA looks at for padding rows: padding comes in runs (an expert's
+// last block, the tail of the list), so a short list takes one slot per CTA
+// (the 120 padding rows of one token's list took 14 us as eight rows a warp,
+// 2 us so), and a long one up to a warp's worth, which keeps the CTAs few.
+int pad_slots(long long cap) {
+  return static_cast<int>(std::max(1ll, std::min(32ll, cap / (152 * 16))));
+}
 
 // A run of V elements of type T, loaded and stored as one word.
 template <int BYTES>
@@ -94,20 +98,21 @@ __device__ __forceinline__ typename Word<sizeof(T) * V>::type pack(const float (
   }
 }
 
-// Zero rows of the padding slots among the kPadSlots slots of job `job`, by
-// one warp.
+// Zero rows of the padding slots among slots [job * per, job * per + per),
+// per <= 32, by one CTA.
 template <typename W>
 __device__ __forceinline__ void zero_padding(const int32_t* __restrict__ sorted_ids, long long job,
-                                             long long cap, int n_assign, int row_words,
-                                             W* __restrict__ rows, int lane) {
-  const long long s0 = job * kPadSlots;
-  const bool pad = lane < kPadSlots && s0 + lane < cap && sorted_ids[s0 + lane] >= n_assign;
+                                             int per, long long cap, int n_assign, int row_words,
+                                             W* __restrict__ rows) {
+  const int lane = threadIdx.x & 31;
+  const long long s0 = job * per;
+  const bool pad = lane < per && s0 + lane < cap && sorted_ids[s0 + lane] >= n_assign;
   unsigned todo = __ballot_sync(0xffffffffu, pad);
   while (todo != 0) {
     const int u = __ffs(todo) - 1;
     todo &= todo - 1;
     W* row = rows + (s0 + u) * row_words;
-    for (int c = lane; c < row_words; c += 32) row[c] = W{};
+    for (int c = threadIdx.x; c < row_words; c += kThreads) row[c] = W{};
   }
 }
 
@@ -115,7 +120,7 @@ __device__ __forceinline__ void zero_padding(const int32_t* __restrict__ sorted_
 // the slots of its K choices.  Jobs after them: padding rows.
 template <typename W>
 __global__ void __launch_bounds__(kThreads)
-    permute_kernel(const W* __restrict__ x, int T, int K, int row_words, int chunks,
+    permute_kernel(const W* __restrict__ x, int T, int K, int row_words, int chunks, int pad_per,
                    const int32_t* __restrict__ inv_perm, const int32_t* __restrict__ sorted_ids,
                    long long cap, W* __restrict__ xs, const int32_t* status) {
   pdl_wait();
@@ -123,9 +128,7 @@ __global__ void __launch_bounds__(kThreads)
   if (status != nullptr && *status != 0) return;
   const long long token_jobs = static_cast<long long>(T) * chunks;
   if (blockIdx.x >= token_jobs) {
-    const int warp = threadIdx.x >> 5;
-    zero_padding(sorted_ids, (blockIdx.x - token_jobs) * kWarps + warp, cap, T * K, row_words, xs,
-                 threadIdx.x & 31);
+    zero_padding(sorted_ids, blockIdx.x - token_jobs, pad_per, cap, T * K, row_words, xs);
     return;
   }
   const int t = static_cast<int>(blockIdx.x / chunks);
@@ -175,12 +178,14 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// A warp per assignment: its dy row and its dw; then padding rows.
+// A warp per assignment, its dy row and its dw; the CTAs from `pad0` on take
+// padding rows.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
     unpermute_backward_kernel(const T* __restrict__ dout_, const T* __restrict__ y_,
                               const float* __restrict__ weights, int n_assign, int K,
-                              int row_words, const int32_t* __restrict__ inv_perm,
+                              int row_words, unsigned pad0, int pad_per,
+                              const int32_t* __restrict__ inv_perm,
                               const int32_t* __restrict__ sorted_ids, long long cap,
                               T* __restrict__ dy_, float* __restrict__ dw,
                               const int32_t* status) {
@@ -188,20 +193,21 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   pdl_launch_dependents();
   if (status != nullptr && *status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const long long job = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   W* dy = reinterpret_cast<W*>(dy_);
-  if (job >= n_assign) {
-    zero_padding(sorted_ids, job - n_assign, cap, n_assign, row_words, dy, lane);
+  if (blockIdx.x >= pad0) {
+    zero_padding(sorted_ids, blockIdx.x - pad0, pad_per, cap, n_assign, row_words, dy);
     return;
   }
+  const int lane = threadIdx.x & 31;
+  const int job = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (job >= n_assign) return;
   const long long slot = inv_perm[job];
   if (slot < 0 || !in_bounds(slot < cap, status)) {
     if (lane == 0) dw[job] = 0.0f;
     return;
   }
   const float w = weights[job];
-  const W* g = reinterpret_cast<const W*>(dout_) + (job / K) * row_words;
+  const W* g = reinterpret_cast<const W*>(dout_) + static_cast<long long>(job / K) * row_words;
   const W* y = reinterpret_cast<const W*>(y_) + slot * row_words;
   dy += slot * row_words;
   float dot = 0.0f;
@@ -228,7 +234,7 @@ int word_bytes(long long row_bytes, const void* a, const void* b, const void* c 
   return static_cast<int>(all & (~all + 1));
 }
 
-long long pad_jobs(long long cap) { return (cap + kPadSlots - 1) / kPadSlots; }
+long long pad_jobs(long long cap, int per) { return (cap + per - 1) / per; }
 
 template <typename W>
 cudaError_t permute_as(const void* x, int T, int K, long long row_bytes, const int32_t* inv_perm,
@@ -236,13 +242,13 @@ cudaError_t permute_as(const void* x, int T, int K, long long row_bytes, const i
                        cudaStream_t s) {
   const int row_words = static_cast<int>(row_bytes / sizeof(W));
   const int chunks = (row_words + kThreads - 1) / kThreads;
-  const long long grid =
-      static_cast<long long>(T) * chunks + (pad_jobs(cap) + kWarps - 1) / kWarps;
+  const int per = pad_slots(cap);
+  const long long grid = static_cast<long long>(T) * chunks + pad_jobs(cap, per);
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, attr);
   return cudaLaunchKernelEx(&cfg, permute_kernel<W>, static_cast<const W*>(x), T, K, row_words,
-                            chunks, inv_perm, sorted_ids, cap, static_cast<W*>(xs), status);
+                            chunks, per, inv_perm, sorted_ids, cap, static_cast<W*>(xs), status);
 }
 
 template <typename T, int V>
@@ -266,13 +272,14 @@ cudaError_t unpermute_backward_as(const void* dout, const void* y, const float* 
                                   int tokens, int K, int H, const int32_t* inv_perm,
                                   const int32_t* sorted_ids, long long cap, void* dy, float* dw,
                                   const int32_t* status, cudaStream_t s) {
-  const long long jobs = static_cast<long long>(tokens) * K + pad_jobs(cap);
-  const unsigned grid = static_cast<unsigned>((jobs + kWarps - 1) / kWarps);
+  const unsigned pad0 = static_cast<unsigned>((tokens * K + kWarps - 1) / kWarps);
+  const int per = pad_slots(cap);
+  const unsigned grid = pad0 + static_cast<unsigned>(pad_jobs(cap, per));
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(kThreads), 0, s, attr);
   return cudaLaunchKernelEx(&cfg, unpermute_backward_kernel<T, V>, static_cast<const T*>(dout),
-                            static_cast<const T*>(y), weights, tokens * K, K, H / V, inv_perm,
-                            sorted_ids, cap, static_cast<T*>(dy), dw, status);
+                            static_cast<const T*>(y), weights, tokens * K, K, H / V, pad0,
+                            per, inv_perm, sorted_ids, cap, static_cast<T*>(dy), dw, status);
 }
 
 }  // namespace
