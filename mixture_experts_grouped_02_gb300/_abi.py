@@ -41,7 +41,7 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_resolve_block_m", "moe_a
            "moe_combine_finish", "moe_forward_noalloc_status", "moe_test_gemm_wait_timeout",
            "moe_gemm1_silu_gather", "moe_permute_tokens", "moe_permute_tokens_backward",
            "moe_unpermute_tokens", "moe_unpermute_tokens_backward", "moe_quantize_fp8_block",
-           "moe_gemm_fp8_block", "moe_grouped_gemm_fp8_block")
+           "moe_gemm_fp8_block", "moe_grouped_gemm_fp8_block", "moe_test_gemm_fp8_block")
 
 MOE_STATIC_SCRATCH_BYTES = 64 << 20
 MOE_ACT_SILU, MOE_ACT_SWIGLU_CLAMP = 0, 1
@@ -168,6 +168,9 @@ def _declare(L):
     L.moe_quantize_fp8_block.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
     L.moe_gemm_fp8_block.restype = i32
     L.moe_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    L.moe_test_gemm_fp8_block.restype = i32
+    L.moe_test_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, i32,
+                                          ctypes.c_ulonglong, vp, vp]
     L.moe_grouped_gemm_fp8_block.restype = i32
     L.moe_grouped_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, i32, i32, sz, i32, vp, vp, vp,
                                              i32, vp, vp]
@@ -422,6 +425,16 @@ def moe_grouped_gemm_fp8_block(a, a_scale, w, w_scale, E, N, K, cap, block_m, bl
                                             block_m, _p(block_info), _p(num_blocks), _p(out),
                                             out_dtype, _p(dev_status), _stream(stream)),
            "moe_grouped_gemm_fp8_block")
+
+
+def moe_test_gemm_fp8_block(a, a_scale, w, w_scale, M, N, K, out, out_dtype, form,
+                            wait_limit_ns=0, dev_status=None, stream=None):
+    """moe_gemm_fp8_block in a given form of its kernel, or with a wait limit
+    its failure path; for tests."""
+    _check(lib().moe_test_gemm_fp8_block(_p(a), _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out),
+                                         out_dtype, int(form), int(wait_limit_ns),
+                                         _p(dev_status), _stream(stream)),
+           "moe_test_gemm_fp8_block")
 
 
 def moe_mx_packed_bytes(E, R, K, sections):

@@ -8,26 +8,52 @@
 // accumulator: the tensor core sums a block (K = 128, four MMAs) into a TMEM
 // buffer of its own, and the epilogue warps multiply it by sa * sb and add it
 // to fp32 registers while the tensor core fills the other buffer.  A row's
-// scale is one register of the thread that owns the row, and a 128-column
-// half of the tile has one weight scale, so this costs one packed
-// fma.rn.f32x2 for two elements.
+// scale is one register of the thread that owns the row (rows of a on the
+// MMA's M side), and the columns of a thread have one weight scale, so this
+// costs one packed fma.rn.f32x2 for two elements.
+//
+// Three forms of one kernel, a template over the weight rows BN of a tile and
+// the mode (fp8b_form chooses, with what each measured):
+//  * kPair: a CTA pair computes 256 rows x 128 weight rows with cta_group::2
+//    MMAs, each CTA holding 128 rows of a and half of the weight rows.  What
+//    an MMA takes is set by the operand bytes it reads from shared memory,
+//    about 75 per clock: M = 128, N = 128 takes 133 clocks on one CTA and 83
+//    as a pair, where each CTA reads half of the weight rows;
+//  * kSingle: one CTA per tile of 128 rows x BN, for lists of small blocks
+//    (weight streaming) and products with too few rows for pairs;
+//  * kSplit: a cluster of 2 to 8 CTAs shares one tile's K range and adds the
+//    partial sums through distributed shared memory, in rank order, for
+//    products with fewer tiles than SMs and a long K.
 //
 // Layout per CTA (one per SM, persistent, tiles walked in bands as in
-// sched.cuh):
-//  * tile = 128 rows of a x 256 weight rows; the columns past N in the last
-//    tile are left out of the MMA's N;
-//  * four stages of one scale block each: A 128 x 128 bytes (16 KB; 32 rows
-//    when the block has at most 32 valid rows), B 256 x 128 bytes (32 KB),
-//    128-byte swizzled, by TMA.  K past the tensor reads as zero codes;
-//  * TMEM: two 256-column fp32 buffers;
-//  * warp 0 TMA, warp 1 MMA, warps 2-9 epilogue: warp w reads the lane
-//    quarter w % 4 and one half of the columns, 128 fp32 sums per thread.
-//    A warp whose 32 rows are all padding only keeps the barriers.
+// sched.cuh; kSplit: one tile per cluster):
+//  * 192 KB of stages of two scale blocks each: A 2 x 128 rows x 128 bytes (32
+//    rows when the row block has at most 32 valid rows), B 2 x BN (kPair:
+//    BN / 2) rows, 128-byte swizzled, by TMA.  K past the tensor reads as
+//    zero codes.  Two blocks to a stage because a handshake costs about as
+//    much as a block's MMAs: a look at an mbarrier 55 clocks and more under
+//    load, a commit until its waiters run 240;
+//  * TMEM: two buffers of two fp32 blocks of BN columns; the columns past N
+//    in the last tile are left out of the MMA's N;
+//  * warp 0 TMA, warp 1 MMA, warp 2 the row scales (loaded by the threads
+//    that need them they took 32 L1 lines per load and warp and held up the
+//    buffers' release, 285 us instead of 218 for 8192 x 4096 x 7168), warps
+//    3-10 epilogue: warp w reads the lane quarter w % 4 and one half of the
+//    columns.  A warp whose 32 rows are all padding only keeps the barriers.
+//
+// 8192 x 4096 x 7168: 202-213 us, 2.3 PFLOP/s.  A stage takes a pair about 790
+// clocks, of which the MMAs are 660; what is left is the chain from the last
+// MMA of a buffer over its epilogue to the next MMA into it (240 + 590 + 225
+// clocks beside the MMAs, over two buffers, all that TMEM holds).
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
 // up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
 // drains and frees its TMEM.
 #include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "bounds.cuh"
 #include "internal.h"
@@ -37,46 +63,142 @@
 namespace moe {
 namespace {
 
+enum Mode { kSingle = 0, kSplit = 1, kPair = 2 };  // Fp8bForm::mode
+
+// Row blocks a pair launch can list (see list_pairs).
+constexpr int kMaxPairs = 4096;
+
+template <int BN_, int MODE>
 struct Cfg {
   static constexpr int kBM = 128;
-  static constexpr int kBN = 256;
-  static constexpr int kBK = 128;
+  static constexpr int kBK = 128;  // one scale block
+  static constexpr int kSub = 2;   // scale blocks of a stage (two units of work)
   static constexpr int kUmmaK = 32;
-  static constexpr int kStages = 4;
+  static constexpr int kBRows = MODE == kPair ? BN_ / 2 : BN_;  // weight rows per CTA
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kAShortRows = 32;
   static constexpr int kAShortBytes = kAShortRows * kBK;
-  static constexpr int kBBytes = kBN * kBK;
-  static constexpr int kTmemCols = 2 * kBN;
+  static constexpr int kBBytes = kBRows * kBK;
+  static constexpr int kStageBytes = kSub * (kABytes + kBBytes);
+  static constexpr int kStages = 192 * 1024 / kStageBytes;
+  // buffers of kSub scale blocks: stage j waits for the epilogue of j - kBufs
+  static constexpr int kBufs = 2;
+  static constexpr int kBufCols = kSub * BN_;
+  static constexpr int kTmemCols = kBufs * kBufCols;
+  static_assert(kStages > kBufs, "the scale slots need a stage more than buffers");
   static constexpr int kMmaWarp = 1;
+  static constexpr int kScaleWarp = 2;
+  static constexpr int kFirstEpi = 3;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = (2 + kEpiWarps) * 32;
-  static constexpr int kSmemBytes = kStages * (kABytes + kBBytes) + 1024;
+  static constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
+  static constexpr int kCols = BN_ / 2;  // columns of an epilogue thread
+  static constexpr int kListBytes = MODE == kPair ? kMaxPairs * 2 : 0;
+  static constexpr int kOutBytes = kEpiWarps * 2048;  // see store_rows
+  static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + kListBytes + 1024;
 };
 
-// Row block `mb` of the call: expert, first row, valid rows.
+// A CTA's part of a tile: expert, first row, valid rows (0: none), and the
+// valid rows of the pair's other CTA.
 struct RowBlock {
-  int e, r0, valid;
+  int e, r0, valid, other;
 };
 
+// Valid rows of part `sub` (128 rows each) of align block `bi`.
+__device__ __forceinline__ int part_valid(const Fp8bArgs& a, const int4& bi, int sub) {
+  if (!block_in_bounds(bi, a.E, a.cap, a.subs * 128, a.status)) return 0;
+  return max(0, min(128, bi.w - 128 * sub));
+}
+
+// Row block `mb` of the call: 128 rows of a plain product, or part of an align
+// block (blocks of 256 rows have two parts).
 __device__ __forceinline__ RowBlock row_block(const Fp8bArgs& a, int mb) {
+  RowBlock r;
+  r.other = 0;
+  if (a.block_info == nullptr) {
+    r.e = 0;
+    r.r0 = mb * 128;
+    r.valid = min(128, a.M - r.r0);
+    return r;
+  }
+  const int b = mb / a.subs, sub = mb - b * a.subs;
+  const int4 bi = reinterpret_cast<const int4*>(a.block_info)[b];
+  r.e = bi.x;
+  r.r0 = bi.z + 128 * sub;
+  r.valid = part_valid(a, bi, sub);
+  return r;
+}
+
+// Row blocks of pair `p`, for the CTA of rank `rank`: 256 rows of a plain
+// product, the two parts of a 256-row align block, or a listed block and the
+// next one of its expert.
+__device__ __forceinline__ RowBlock pair_block(const Fp8bArgs& a, int p, int rank,
+                                               const uint16_t* list) {
   RowBlock r;
   if (a.block_info == nullptr) {
     r.e = 0;
-    r.r0 = mb * Cfg::kBM;
-    r.valid = min(Cfg::kBM, a.M - r.r0);
+    r.r0 = p * 256 + 128 * rank;
+    r.valid = max(0, min(128, a.M - r.r0));
+    r.other = max(0, min(128, a.M - p * 256 - 128 * (rank ^ 1)));
     return r;
   }
-  // align blocks of up to 256 rows are read as `subs` row blocks
-  const int b = mb / a.subs;
-  const int4 bi = reinterpret_cast<const int4*>(a.block_info)[b];
-  const int off = (mb - b * a.subs) * Cfg::kBM;
-  r.e = bi.x;
-  r.r0 = bi.z + off;
-  r.valid = block_in_bounds(bi, a.E, a.cap, a.subs * Cfg::kBM, a.status)
-                ? max(0, min(Cfg::kBM, bi.w - off))
-                : 0;
+  const int4* info = reinterpret_cast<const int4*>(a.block_info);
+  if (a.subs == 2) {
+    const int4 bi = info[p];
+    r.e = bi.x;
+    r.r0 = bi.z + 128 * rank;
+    r.valid = part_valid(a, bi, rank);
+    r.other = part_valid(a, bi, rank ^ 1);
+    return r;
+  }
+  const int b = list[p] >> 1;
+  const bool two = list[p] & 1;
+  const int4 b0 = info[b];
+  const int v0 = part_valid(a, b0, 0);
+  int4 b1 = b0;
+  int v1 = 0;
+  if (two) {
+    b1 = info[b + 1];
+    v1 = part_valid(a, b1, 0);
+  }
+  r.e = b0.x;
+  r.r0 = rank == 0 ? b0.z : b1.z;
+  r.valid = rank == 0 ? v0 : v1;
+  r.other = rank == 0 ? v1 : v0;
   return r;
+}
+
+// The pairs of a list of `nb` align blocks of at most 128 rows: every block of
+// even index within its expert, with the next one where the expert has it.
+// Entry = 2 * block + (has a second one); at most kMaxPairs blocks.  All threads of the CTA; returns
+// the number of pairs.
+__device__ __forceinline__ int list_pairs(const Fp8bArgs& a, int nb, uint16_t* list,
+                                          int* s_warp_sum) {
+  const int4* info = reinterpret_cast<const int4*>(a.block_info);
+  const int per = (nb + blockDim.x - 1) / blockDim.x;
+  const int lo = min(nb, static_cast<int>(threadIdx.x) * per), hi = min(nb, lo + per);
+  int cnt = 0;
+  for (int b = lo; b < hi; ++b) cnt += (info[b].y & 1) == 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = cnt;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) s_warp_sum[warp] = incl;
+  __syncthreads();
+  int at = incl - cnt, total = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+    if (w < warp) at += s_warp_sum[w];
+    total += s_warp_sum[w];
+  }
+  for (int b = lo; b < hi; ++b) {
+    const int m = info[b].y;
+    if (m & 1) continue;
+    const bool two = b + 1 < nb && info[b + 1].y == m + 1;
+    list[at++] = static_cast<uint16_t>(2 * b + (two ? 1 : 0));
+  }
+  return total;
 }
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -96,79 +218,119 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
-// 128 sums of a row to columns [col, col + 128) of out, those below N.
-__device__ __forceinline__ void store_row(const Fp8bArgs& a, long long row, int col,
-                                          const uint64_t (&acc)[64]) {
-  const int n = min(128, a.N - col);
-  if (a.out_bf16) {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row * a.N + col;
-    if (a.wide_out) {
+// The COLS sums of each of a warp's 32 rows (a lane per row) to columns
+// [col, col + COLS) of out, those below N, for the first `rows` rows.  16-byte
+// stores go through `stage`, 2 KB of shared memory of the warp: 64 bytes of
+// every row at a time are written there by the row's lane, in 16-byte pieces
+// rotated by the row so that neither side meets a bank twice, and read back
+// four lanes to a row, so that a store covers 8 rows of 64 bytes instead of 32
+// of 16.  (Stored straight from the rows' lanes, a tile's output kept the
+// epilogue 3700 clocks from its next tile.)
+template <int COLS>
+__device__ __forceinline__ void store_rows(const Fp8bArgs& a, long long row0, int rows, int col,
+                                           const uint64_t (&acc)[COLS / 2], uint4* stage,
+                                           int lane) {
+  const int n = min(COLS, a.N - col);
+  const int es = a.out_bf16 ? 2 : 4;
+  if (!a.wide_out) {
+    if (lane >= rows) return;
+    const long long o = (row0 + lane) * a.N + col;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (8 * i < n) {
-          uint32_t p[4];
+    for (int i = 0; i < COLS / 2; ++i) {
+      float v[2];
+      unpack2(acc[i], v[0], v[1]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float lo, hi;
-            unpack2(acc[4 * i + j], lo, hi);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-            p[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          reinterpret_cast<uint4*>(o)[i] = make_uint4(p[0], p[1], p[2], p[3]);
+      for (int j = 0; j < 2; ++j) {
+        if (2 * i + j < n) {
+          if (a.out_bf16)
+            static_cast<__nv_bfloat16*>(a.out)[o + 2 * i + j] = __float2bfloat16_rn(v[j]);
+          else
+            static_cast<float*>(a.out)[o + 2 * i + j] = v[j];
         }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        float lo, hi;
-        unpack2(acc[i], lo, hi);
-        if (2 * i < n) o[2 * i] = __float2bfloat16_rn(lo);
-        if (2 * i + 1 < n) o[2 * i + 1] = __float2bfloat16_rn(hi);
       }
     }
     return;
   }
-  float* o = static_cast<float*>(a.out) + row * a.N + col;
-  if (a.wide_out) {
+  char* base = static_cast<char*>(a.out) + (row0 * a.N + col) * es;
+  const long long pitch = static_cast<long long>(a.N) * es;
+  const int rd_row = lane >> 2, piece = lane & 3;
+  // 64 bytes of the rows from sum 16 c (fp32) or 32 c (bf16) on
+  auto flush = [&](int c) {
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (4 * i < n) {
-        float4 v;
-        unpack2(acc[2 * i], v.x, v.y);
-        unpack2(acc[2 * i + 1], v.z, v.w);
-        reinterpret_cast<float4*>(o)[i] = v;
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + rd_row;
+      const uint4 v = stage[4 * r + ((piece + (r >> 1)) & 3)];
+      if (r < rows && (64 * c + 16 * piece) < n * es)
+        *reinterpret_cast<uint4*>(base + r * pitch + 64 * c + 16 * piece) = v;
+    }
+    __syncwarp();
+  };
+  if (a.out_bf16) {
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          unpack2(acc[16 * c + 4 * g + j], lo, hi);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+          p[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        stage[4 * lane + ((g + (lane >> 1)) & 3)] = make_uint4(p[0], p[1], p[2], p[3]);
       }
+      flush(c);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      float lo, hi;
-      unpack2(acc[i], lo, hi);
-      if (2 * i < n) o[2 * i] = lo;
-      if (2 * i + 1 < n) o[2 * i + 1] = hi;
+    for (int c = 0; c < COLS / 16; ++c) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float v[4];
+        unpack2(acc[8 * c + 2 * g], v[0], v[1]);
+        unpack2(acc[8 * c + 2 * g + 1], v[2], v[3]);
+        stage[4 * lane + ((g + (lane >> 1)) & 3)] =
+            make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3]));
+      }
+      flush(c);
     }
   }
 }
 
-__global__ void __launch_bounds__(Cfg::kThreads, 1)
+template <int BN, int MODE>
+__global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
     fp8b_gemm_kernel(const __grid_constant__ Fp8bArgs a, const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmAShort,
                      const __grid_constant__ CUtensorMap tmB) {
-  using C = Cfg;
+  using C = Cfg<BN, MODE>;
+  constexpr bool PAIR = MODE == kPair;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::kStages];
   __shared__ __align__(8) uint64_t empty_bar[C::kStages];
-  __shared__ __align__(8) uint64_t accf_bar[2];
-  __shared__ __align__(8) uint64_t acce_bar[2];
+  __shared__ __align__(8) uint64_t acce_bar[C::kBufs];
+  __shared__ __align__(8) uint64_t scale_bar[C::kStages];
+  // sa * sb of the tile's rows for the scale blocks of each stage
+  __shared__ float s_scale[C::kStages][C::kSub][128];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_skip;
+  __shared__ int s_warp_sum[C::kThreads / 32];
   __shared__ volatile int s_abort;
 
-  const int warp = threadIdx.x >> 5;
+  // through a shuffle, so that the compiler knows it to be the same for a warp
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = MODE == kSingle ? 0u : cluster_ctarank();
+  const bool leader = !PAIR || rank == 0;
   const uint32_t smemA = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t smemB = smemA + C::kStages * C::kABytes;
+  const uint32_t smemB = smemA + C::kStages * C::kSub * C::kABytes;
+  uint8_t* smem_gen = smem_raw + (smemA - smem_u32(smem_raw));
+  uint4* out_stage = reinterpret_cast<uint4*>(smem_gen + C::kStages * C::kStageBytes);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem_gen + C::kStages * C::kStageBytes +
+                                               C::kOutBytes);
 
   pdl_wait();
   pdl_launch_dependents();
@@ -176,197 +338,561 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     s_skip = (a.status != nullptr && *reinterpret_cast<volatile int32_t*>(a.status) != 0);
     s_abort = 0;
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(smem_u32(&full_bar[i]), 1);
+      // the expected bytes and (one CTA: see the scale warp) the scales
+      mbar_init(smem_u32(&full_bar[i]), PAIR ? 1 : 2);
+      mbar_init(smem_u32(&scale_bar[i]), 1);
       mbar_init(smem_u32(&empty_bar[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&accf_bar[i]), 1);
-      mbar_init(smem_u32(&acce_bar[i]), C::kEpiWarps);
-    }
+    for (int i = 0; i < C::kBufs; ++i)
+      mbar_init(smem_u32(&acce_bar[i]), (PAIR ? 2 : 1) * C::kEpiWarps);
     mbar_init(smem_u32(&drain_bar), 1);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  __syncthreads();
-  if (s_skip) return;
-  if (warp == C::kMmaWarp) tmem_alloc(smem_u32(&s_tmem_base), C::kTmemCols);
+  if constexpr (MODE == kSingle) {
+    __syncthreads();
+  } else {
+    cluster_sync();
+  }
+  // one answer per cluster: the status word may change while its CTAs start
+  const bool skip =
+      (MODE == kSingle ? s_skip
+                       : static_cast<int>(ld_shared_cluster_u32(
+                             mapa_shared(smem_u32(&s_skip), 0)))) != 0;
+  if (!skip && warp == C::kMmaWarp) {
+    if constexpr (PAIR)
+      tmem_alloc_pair(smem_u32(&s_tmem_base), C::kTmemCols);
+    else
+      tmem_alloc(smem_u32(&s_tmem_base), C::kTmemCols);
+  }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmAShort);
     tma_prefetch_desc(&tmB);
+  }
+  int num_blocks = 0;  // row blocks, or pairs of them
+  if (!skip) {
+    if (a.block_info == nullptr) {
+      num_blocks = PAIR ? (a.max_blocks + 1) / 2 : a.max_blocks;
+    } else {
+      num_blocks = checked_num_blocks(*a.num_blocks, a.max_blocks, a.status);
+      if constexpr (PAIR) {
+        if (a.subs == 1) num_blocks = list_pairs(a, num_blocks, list, s_warp_sum);
+      } else {
+        num_blocks *= a.subs;
+      }
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = s_tmem_base;
 
-  const int num_blocks =
-      a.block_info == nullptr
-          ? a.max_blocks
-          : checked_num_blocks(*a.num_blocks, a.max_blocks, a.status) * a.subs;
   const int total = num_blocks * a.n_tiles;
+  const int csize = MODE == kSingle ? 1 : (PAIR ? 2 : a.splits);
+  const int first = blockIdx.x / csize;
+  const int step = gridDim.x / csize;
+  // this CTA's scale blocks
+  const int kb = MODE == kSplit ? a.k_tiles * static_cast<int>(rank) / a.splits : 0;
+  const int ke = MODE == kSplit ? a.k_tiles * (static_cast<int>(rank) + 1) / a.splits : a.k_tiles;
   const uint64_t to = a.timeout_ns;
 
-  if (warp == 0) {
-    // ------------------------------------------------------- TMA producer
-    if (lane == 0 && !a.starve) {
-      uint32_t stage = 0, phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const Tile t = decode_tile(tile, num_blocks, a);
-        const RowBlock r = row_block(a, t.mb);
-        if (r.valid <= 0) continue;
-        const bool short_a = r.valid <= C::kAShortRows;
-        const uint32_t tx = C::kBBytes + (short_a ? C::kAShortBytes : C::kABytes);
-        const int w_row = r.e * a.N + t.nt * C::kBN;
-        for (int kt = 0; kt < a.k_tiles; ++kt) {
-          if (!mbar_wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1, &s_abort, to)) {
-            ok = false;
-            break;
+  auto block_of = [&](int mb) {
+    if constexpr (PAIR)
+      return pair_block(a, mb, static_cast<int>(rank), list);
+    else
+      return row_block(a, mb);
+  };
+  // MMA columns of weight tile nt: a multiple of 16
+  auto tile_cols = [&](int nt) { return min(BN, (a.N - nt * BN + 15) & ~15); };
+  auto live_tile = [&](const RowBlock& r) { return r.valid > 0 || r.other > 0; };
+
+  if (warp < C::kFirstEpi) {
+    if (warp == 0) {
+      // ----------------------------------------------------- TMA producer
+      // (a.starve, the failure-path test: no copies at all)
+      if (elect_one() && !a.starve) {
+        uint32_t stage = 0, phase = 0;
+        unsigned issued = 0;
+        bool ok = true;
+        const uint32_t full0 =
+            PAIR ? mapa_shared(smem_u32(&full_bar[0]), 0) : smem_u32(&full_bar[0]);
+        for (int tile = first; tile < total && ok; tile += step) {
+          const Tile t = decode_tile(tile, num_blocks, a);
+          const RowBlock r = block_of(t.mb);
+          if (!live_tile(r)) continue;
+          auto a_bytes = [&](int valid) {
+            return valid <= C::kAShortRows ? C::kAShortBytes : C::kABytes;
+          };
+          const CUtensorMap* map_a = r.valid <= C::kAShortRows ? &tmAShort : &tmA;
+          const uint32_t tx = PAIR ? 2 * C::kBBytes + a_bytes(r.valid) + a_bytes(r.other)
+                                   : C::kBBytes + a_bytes(r.valid);
+          // (kPair: this CTA's half of the tile's weight rows)
+          const int w_row = r.e * a.N + t.nt * BN +
+                            (PAIR ? static_cast<int>(rank) * (tile_cols(t.nt) >> 1) : 0);
+          for (int kt = kb; kt < ke; kt += C::kSub) {
+            if (!mbar_wait_suspend(smem_u32(&empty_bar[stage]), phase ^ 1, &s_abort, to)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = full0 + stage * 8u;
+            const int nk = min(C::kSub, ke - kt);
+            if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), tx * nk);
+            for (int u = 0; u < nk; ++u) {
+              const uint32_t da = smemA + (stage * C::kSub + u) * C::kABytes;
+              const uint32_t db = smemB + (stage * C::kSub + u) * C::kBBytes;
+              if constexpr (PAIR) {
+                tma_load_2d_pair(da, map_a, fb, (kt + u) * C::kBK, r.r0);
+                tma_load_2d_pair(db, &tmB, fb, (kt + u) * C::kBK, w_row);
+              } else {
+                tma_load_2d(da, map_a, fb, (kt + u) * C::kBK, r.r0);
+                tma_load_2d(db, &tmB, fb, (kt + u) * C::kBK, w_row);
+              }
+            }
+            ++issued;
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-          const uint32_t fb = smem_u32(&full_bar[stage]);
-          mbar_arrive_expect_tx(fb, tx);
-          tma_load_2d(smemA + stage * C::kABytes, short_a ? &tmAShort : &tmA, fb, kt * C::kBK,
-                      r.r0);
-          tma_load_2d(smemB + stage * C::kBBytes, &tmB, fb, kt * C::kBK, w_row);
-          ++issued;
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1;
+        }
+        if (!ok) {
+          if constexpr (PAIR) {
+            settle(to / 8);
+          } else {
+            const unsigned n0 = issued > C::kStages ? issued - C::kStages : 0;
+            for (unsigned n = n0; n < issued; ++n)
+              drain_wait(smem_u32(&full_bar[n % C::kStages]), (n / C::kStages) & 1, to / 4);
           }
         }
       }
-      if (!ok) {
-        const long long first = issued > C::kStages ? issued - C::kStages : 0;
-        for (long long n = first; n < issued; ++n)
-          drain_wait(smem_u32(&full_bar[n % C::kStages]),
-                     static_cast<uint32_t>((n / C::kStages) & 1), to / 4);
-      }
-    }
-    __syncwarp();
-  } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    } else if (warp == C::kMmaWarp && leader && elect_one()) {
+      // ----------------------------------------------------- MMA issuer
+      // stage 0's descriptors; their address field counts 16 bytes
+      const uint64_t a_desc0 = sw128_kmajor_desc(smemA), b_desc0 = sw128_kmajor_desc(smemB);
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = first; tile < total && ok; tile += step) {
         const Tile t = decode_tile(tile, num_blocks, a);
-        if (row_block(a, t.mb).valid <= 0) continue;
-        const int n = min(C::kBN, (a.N - t.nt * C::kBN + 15) & ~15);
-        const uint32_t idesc = make_idesc(0, C::kBM, n);  // e4m3 x e4m3
-        for (int kt = 0; kt < a.k_tiles; ++kt) {
-          if (!mbar_wait_bounded(smem_u32(&acce_bar[buf]), buf_phase ^ 1, &s_abort, to) ||
-              !mbar_wait_bounded(smem_u32(&full_bar[stage]), phase, &s_abort, to)) {
+        if (!live_tile(block_of(t.mb))) continue;
+        const uint32_t idesc = make_idesc(0, PAIR ? 256 : 128, tile_cols(t.nt));  // e4m3 x e4m3
+        for (int kt = kb; kt < ke; kt += C::kSub) {
+          // both looks in flight at once
+          const uint32_t bf = smem_u32(&full_bar[stage]);
+          const uint32_t be = smem_u32(&acce_bar[buf]);
+          const bool rf = mbar_look<PAIR>(bf, phase);
+          const bool re = mbar_look<PAIR>(be, buf_phase ^ 1);
+          const uint32_t d_tmem = tmem_base + buf * C::kBufCols;
+          const uint64_t ad = a_desc0 + stage * (C::kSub * C::kABytes >> 4);
+          const uint64_t bd = b_desc0 + stage * (C::kSub * C::kBBytes >> 4);
+          auto mma = [&](int u) {
+#pragma unroll
+            for (int k = 0; k < C::kBK / C::kUmmaK; ++k) {
+              const uint64_t da = ad + u * (C::kABytes >> 4) + k * (C::kUmmaK >> 4);
+              const uint64_t db = bd + u * (C::kBBytes >> 4) + k * (C::kUmmaK >> 4);
+              if constexpr (PAIR)
+                umma_f8_pair(d_tmem + u * BN, da, db, idesc, k > 0 ? 1u : 0u);
+              else
+                umma_f8(d_tmem + u * BN, da, db, idesc, k > 0 ? 1u : 0u);
+            }
+          };
+          auto commit = [&](uint32_t bar) {
+            if constexpr (PAIR)
+              umma_commit_pair(bar, 0x3);
+            else
+              umma_commit(bar);
+          };
+          if (!(rf || mbar_wait_suspended<PAIR>(bf, phase, &s_abort, to)) ||
+              !(re || mbar_wait_suspended<PAIR>(be, buf_phase ^ 1, &s_abort, to))) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a_base = smemA + stage * C::kABytes;
-          const uint32_t b_base = smemB + stage * C::kBBytes;
-          const uint32_t d_tmem = tmem_base + buf * C::kBN;
-#pragma unroll
-          for (int k = 0; k < C::kBK / C::kUmmaK; ++k)
-            umma_f8(d_tmem, sw128_kmajor_desc(a_base + k * C::kUmmaK),
-                    sw128_kmajor_desc(b_base + k * C::kUmmaK), idesc, k > 0 ? 1u : 0u);
-          umma_commit(smem_u32(&empty_bar[stage]));
-          umma_commit(smem_u32(&accf_bar[buf]));
+          mma(0);
+          if (kt + 1 < ke) mma(1);
+          // frees the stage and hands the buffer to the epilogue
+          commit(smem_u32(&empty_bar[stage]));
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1;
           }
-          buf ^= 1;
-          if (buf == 0) buf_phase ^= 1;
+          if (++buf == C::kBufs) {
+            buf = 0;
+            buf_phase ^= 1;
+          }
         }
       }
       if (!ok) {
-        umma_commit(smem_u32(&drain_bar));
+        if constexpr (PAIR)
+          umma_commit_pair(smem_u32(&drain_bar), 0x1);
+        else
+          umma_commit(smem_u32(&drain_bar));
         drain_wait(smem_u32(&drain_bar), 0, to / 4);
+      }
+    } else if (warp == C::kScaleWarp && !a.starve) {
+      // ----------------------------------------------------- scales
+      // A lane has four rows; a stage's scale blocks are loaded while those
+      // of the stage before it are written.  Stage j takes the slot of stage
+      // j - kStages, which the epilogue has read once the MMAs of stage
+      // j - kStages + kBufs are done (they wait for its buffer).
+      uint32_t stage = 0;
+      int w_stage = C::kBufs % C::kStages;  // of stage j - kStages + kBufs
+      uint32_t w_phase = 0;
+      int fresh = C::kStages;  // slots not used before
+      bool ok = true;
+      for (int tile = first; tile < total && ok; tile += step) {
+        const Tile t = decode_tile(tile, num_blocks, a);
+        const RowBlock r = block_of(t.mb);
+        if (!live_tile(r)) continue;
+        const float* sb = a.w_scale + (static_cast<long long>(r.e) * a.n_scales +
+                                       t.nt * BN / 128) * a.k_tiles;
+        const float* sa = a.a_scale + (static_cast<long long>(r.r0) + lane) * a.k_tiles;
+        const long long row32 = 32ll * a.k_tiles;
+        float na[C::kSub][4], nb[C::kSub];
+        auto load = [&](int kt) {
+#pragma unroll
+          for (int u = 0; u < C::kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              na[u][i] = kt + u < ke && lane + 32 * i < r.valid ? __ldg(sa + i * row32 + kt + u)
+                                                                : 0.0f;
+            nb[u] = kt + u < ke ? __ldg(sb + kt + u) : 0.0f;
+          }
+        };
+        load(kb);
+        for (int kt = kb; kt < ke; kt += C::kSub) {
+          float s[C::kSub][4];
+#pragma unroll
+          for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][i] = na[u][i] * nb[u];
+          load(kt + C::kSub);
+          if (fresh > 0) {
+            --fresh;
+          } else {
+            const int good =
+                mbar_wait_suspend(smem_u32(&empty_bar[w_stage]), w_phase, &s_abort, to);
+            if (!__all_sync(0xffffffffu, good)) {
+              ok = false;
+              break;
+            }
+            if (++w_stage == C::kStages) {
+              w_stage = 0;
+              w_phase ^= 1;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_scale[stage][u][32 * i + lane] = s[u][i];
+          // One CTA: the slot joins its stage's full barrier, and whoever
+          // sees that stage's MMAs done sees it too.  A pair's full barrier
+          // is the leader's alone: a barrier of its own.
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(PAIR ? &scale_bar[stage] : &full_bar[stage]));
+          if (++stage == C::kStages) stage = 0;
+        }
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;
-    uint32_t buf = 0, buf_phase = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    const int col_in_tile = ((warp - C::kFirstEpi) >> 2) * C::kCols;
+    const uint32_t acce0 =
+        PAIR ? mapa_shared(smem_u32(&acce_bar[0]), 0) : smem_u32(&acce_bar[0]);
+    uint32_t buf = 0, stage = 0, phase = 0;
+    for (int tile = first; tile < total; tile += step) {
       const Tile t = decode_tile(tile, num_blocks, a);
-      const RowBlock r = row_block(a, t.mb);
-      if (r.valid <= 0) continue;
+      const RowBlock r = block_of(t.mb);
+      if (!live_tile(r)) continue;
       const int local = q * 32 + lane;
       const long long row = r.r0 + local;
       const bool row_ok = local < r.valid;
-      const int col = t.nt * C::kBN + half * 128;
+      const int col = t.nt * BN + col_in_tile;
       // warps without a row or a column of the output only keep the barriers
       const bool live = q * 32 < r.valid && col < a.N;
-      const float* sa = a.a_scale + (row_ok ? row : r.r0) * a.k_tiles;
-      const float* sb = a.w_scale +
-                        (static_cast<long long>(r.e) * a.n_scales +
-                         min(col, a.N - 1) / 128) * a.k_tiles;
-      uint64_t acc[64];
+      uint64_t acc[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float s_next = live ? __ldg(sa) * __ldg(sb) : 0.0f;
-      for (int kt = 0; kt < a.k_tiles; ++kt) {
-        const uint32_t s_bits = __float_as_uint(s_next);
-        if (live && kt + 1 < a.k_tiles) s_next = __ldg(sa + kt + 1) * __ldg(sb + kt + 1);
-        const int good = mbar_wait_bounded(smem_u32(&accf_bar[buf]), buf_phase, &s_abort, to);
-        if (!__all_sync(0xffffffffu, good)) {
-          ok = false;
-          break;
-        }
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
+      // Waits for a stage's MMAs: its products are in TMEM.  After a wait that
+      // ran out the loop goes on to its end without waiting, so that the warp
+      // stays converged; nothing is stored then.
+      auto wait = [&] {
+        const uint32_t bd = smem_u32(&empty_bar[stage]), bs = smem_u32(&scale_bar[stage]);
+        const bool r0 = mbar_look<false>(bd, phase);
+        const bool r1 = !PAIR || mbar_look<false>(bs, phase);
+        if (!r0) mbar_wait_suspended<false>(bd, phase, &s_abort, to);
+        if (!r1) mbar_wait_suspended<false>(bs, phase, &s_abort, to);
+        __syncwarp();
         tc_fence_after_sync();
-        if (live) {
-          const uint64_t s2 = pack2(s_bits, s_bits);
-          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                 buf * C::kBN + half * 128;
+      };
+      auto release = [&] {
+        tc_fence_before_sync();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_cluster_relaxed(acce0 + buf * 8u);
+          else
+            mbar_arrive_relaxed(acce0 + buf * 8u);
+        }
+      };
+      auto next_stage = [&] {
+        buf ^= 1;
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      if (!live) {
+        for (int kt = kb; kt < ke; kt += C::kSub) {
+          wait();
+          release();
+          next_stage();
+        }
+      } else if (kb < ke) {
+        // Chunks of 32 columns: one is added while another one loads.  A load
+        // takes about 110 clocks, an addition of 16 packed FMAs about 100 with
+        // two warps per scheduler.  The buffer goes back once its last chunk
+        // is in registers.
+        constexpr int kChunks = C::kCols / 32;
+        uint32_t va[32], vb[32];
+        uint64_t s2;
+        auto load = [&](int u, int j, uint32_t(&v)[32]) {
+          tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * C::kBufCols +
+                        u * BN + col_in_tile + 32 * j,
+                    v);
+        };
+        auto scale = [&](int u) {
+          const uint32_t s = __float_as_uint(s_scale[stage][u][local]);
+          s2 = pack2(s, s);
+        };
+        auto add = [&](int j, const uint32_t(&v)[32]) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(taddr + 32 * c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              acc[16 * c + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), s2, acc[16 * c + i]);
+          for (int i = 0; i < 16; ++i)
+            acc[16 * j + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), s2, acc[16 * j + i]);
+        };
+        if constexpr (kChunks == 2) {
+          wait();
+          scale(0);
+          load(0, 0, va);
+          for (int kt = kb; kt < ke; kt += C::kSub) {
+            tmem_wait_ld32(va);
+            load(0, 1, vb);
+            add(0, va);
+            tmem_wait_ld32(vb);
+            if (kt + 1 < ke) {
+              load(1, 0, va);
+              add(1, vb);
+              scale(1);
+              tmem_wait_ld32(va);
+              load(1, 1, vb);
+              add(0, va);
+              tmem_wait_ld32(vb);
+            }
+            release();
+            next_stage();
+            if (kt + C::kSub < ke) {
+              wait();
+              load(0, 0, va);
+            }
+            add(1, vb);
+            if (kt + C::kSub < ke) scale(0);
+          }
+        } else {
+          for (int kt = kb; kt < ke; kt += C::kSub) {
+            wait();
+            scale(0);
+            load(0, 0, va);
+            tmem_wait_ld32(va);
+            if (kt + 1 < ke) {
+              add(0, va);
+              scale(1);
+              load(1, 0, va);
+              tmem_wait_ld32(va);
+            }
+            release();
+            add(0, va);
+            next_stage();
           }
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&acce_bar[buf]));
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1;
       }
-      if (ok && live && row_ok) store_row(a, row, col, acc);
+      if constexpr (MODE == kSplit) {
+        // partial sums, column-major, over the stages (all read by now)
+        float* part = reinterpret_cast<float*>(smem_gen) + col_in_tile * 128 + local;
+        if (live && row_ok) {
+#pragma unroll
+          for (int i = 0; i < C::kCols / 2; ++i) {
+            float lo, hi;
+            unpack2(acc[i], lo, hi);
+            part[(2 * i) * 128] = lo;
+            part[(2 * i + 1) * 128] = hi;
+          }
+        }
+      } else {
+        if (live && !s_abort)
+          store_rows<C::kCols>(a, r.r0 + q * 32, min(32, r.valid - q * 32), col, acc,
+                               out_stage + (warp - C::kFirstEpi) * 128, lane);
+      }
     }
   }
 
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (MODE != kSingle) cluster_sync();
+  if constexpr (MODE == kSplit) {
+    // the cluster's tile: each CTA adds up and stores 64 / splits of its
+    // columns, the partial sums in rank order
+    if (first < total && !s_abort) {
+      const Tile t = decode_tile(first, num_blocks, a);
+      const RowBlock r = block_of(t.mb);
+      const int span = BN / a.splits;
+      const int c0 = static_cast<int>(rank) * span;
+      for (int i = threadIdx.x; i < span * r.valid; i += blockDim.x) {
+        const int c = c0 + i % span, m = i / span;
+        const int col = t.nt * BN + c;
+        if (col >= a.N) continue;
+        float sum = 0.0f;
+        for (int p = 0; p < a.splits; ++p)
+          sum += __uint_as_float(
+              ld_shared_cluster_u32(mapa_shared(smemA, p) + 4u * (c * 128 + m)));
+        const long long o = static_cast<long long>(r.r0 + m) * a.N + col;
+        if (a.out_bf16)
+          static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(sum);
+        else
+          static_cast<float*>(a.out)[o] = sum;
+      }
+    }
+    cluster_sync();  // the peers have read this CTA's shared memory
+  }
   if (threadIdx.x == 0 && s_abort) report_error(a.status, MOE_ERR_TIMEOUT);
-  if (warp == C::kMmaWarp) {
+  if (!skip && warp == C::kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, C::kTmemCols);
+    else
+      tmem_dealloc(tmem_base, C::kTmemCols);
   }
 }
 
+template <int BN, int MODE>
+cudaError_t prepare_kernel() {
+  // once per device: the attribute outlives the launch
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(fp8b_gemm_kernel<BN, MODE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<BN, MODE>::kSmemBytes);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
+template <int BN, int MODE>
+cudaError_t launch(Fp8bArgs a, const Fp8bForm& f, const Fp8bMaps& maps, cudaStream_t s) {
+  using C = Cfg<BN, MODE>;
+  cudaError_t err = prepare_kernel<BN, MODE>();
+  if (err != cudaSuccess) return err;
+  a.n_tiles = (a.N + BN - 1) / BN;
+  a.band = std::min(a.n_tiles, 8);
+  a.splits = f.splits;
+  cudaLaunchAttribute attr[2];
+  const unsigned cluster = MODE == kPair ? 2 : MODE == kSplit ? f.splits : 1;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(dim3(f.grid), dim3(C::kThreads), C::kSmemBytes, s, attr, cluster);
+  return cudaLaunchKernelEx(&cfg, fp8b_gemm_kernel<BN, MODE>, a, maps.a, maps.a_short, maps.b);
+}
+
+long long div_up(long long a, long long b) { return (a + b - 1) / b; }
+
 }  // namespace
 
-cudaError_t launch_fp8b_gemm(Fp8bArgs a, const CUtensorMap& tmA, const CUtensorMap& tmAShort,
-                             const CUtensorMap& tmB, int sms, cudaStream_t s) {
-  using C = Cfg;
-  a.n_tiles = (a.N + C::kBN - 1) / C::kBN;
-  a.band = a.n_tiles < 8 ? a.n_tiles : 8;
-  const long long tiles = static_cast<long long>(a.max_blocks) * a.subs * a.n_tiles;
-  if (tiles > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t err = cudaFuncSetAttribute(
-      fp8b_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (err != cudaSuccess) return err;
-  const int grid = static_cast<int>(tiles < sms ? tiles : sms);
+// CTA pairs of the pair form the current device holds at once, 0 if unknown.
+int fp8b_max_pairs() {
+  using C = Cfg<128, kPair>;
+  if (prepare_kernel<128, kPair>() != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, attr);
-  return cudaLaunchKernelEx(&cfg, fp8b_gemm_kernel, a, tmA, tmAShort, tmB);
+  const cudaLaunchConfig_t cfg =
+      pdl_config(dim3(2), dim3(C::kThreads), C::kSmemBytes, nullptr, attr, 2);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8b_gemm_kernel<128, kPair>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// The form with the least estimated time: rounds of tiles times what a stage
+// takes (GB300, us: 0.40 with 64 weight rows, 0.59 with 128, 0.52 for a pair;
+// 8192 x 4096 x 7168 took 305, 232 and 202).  Measured around the choice:
+// 333 x 2880 x 2880 in 8.4 us with 64 rows, 12 with 128 and 13 as pairs; 1024 x
+// 4096 x 7168 in 47, 36 and 34; 8192 rows of 32 experts against 4096 x 7168 in
+// 407, 300 and 344 (a pair's second half is often padding there).  A sorted
+// list's row blocks are estimated from its capacity: at least one row per
+// align block and all but the padding of E blocks; half a block of padding per
+// expert that has rows.
+Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, int pairs) {
+  Fp8bForm f;
+  f.splits = 1;
+  const long long n64 = div_up(a.N, 64), n128 = div_up(a.N, 128);
+  const long long max_blocks = static_cast<long long>(a.max_blocks) * a.subs;
+  double blocks = static_cast<double>(max_blocks), two = static_cast<double>(div_up(max_blocks, 2));
+  const bool can_pair = pairs > 0 && (a.block_info == nullptr || a.subs == 2 ||
+                                      a.max_blocks <= kMaxPairs);
+  if (a.block_info != nullptr) {
+    const long long rows =
+        std::max<long long>(a.max_blocks, a.cap - static_cast<long long>(a.E) * (a.block_m - 1));
+    const double experts = static_cast<double>(std::min<long long>(a.E, rows));
+    const double part = std::min(128, a.block_m);
+    blocks = std::min(blocks, rows / part + experts / 2);
+    two = a.block_m < 128 ? blocks : std::min(blocks, rows / 256.0 + experts / 2);
+  }
+  auto rounds = [](double tiles, int at_once) { return std::ceil(tiles / at_once); };
+  const double us64 = 0.40 * rounds(blocks * n64, sms);
+  const double us128 = 0.59 * rounds(blocks * n128, sms);
+  const double us_pair = can_pair ? 0.52 * rounds(two * n128, pairs) : 1e30;
+  const long long pair_tiles =
+      (a.block_info != nullptr && a.subs == 1 ? max_blocks : div_up(max_blocks, 2)) * n128;
+  if (us_pair <= us64 && us_pair <= us128) {
+    f.bn = 128;
+    f.mode = kPair;
+    f.grid = static_cast<int>(2 * std::min<long long>(pairs, pair_tiles));
+  } else if (us128 <= us64) {
+    f.bn = 128;
+    f.mode = kSingle;
+    f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n128));
+  } else {
+    f.bn = 64;
+    f.mode = kSingle;
+    f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n64));
+    // Splitting K costs about 3.5 us of cluster launch, barriers and joining:
+    // for one round of tiles with at least 12 stages fewer per CTA (1 x 576 x
+    // 7168: 11.2 us whole, 9.3, 7.4 and 6.8 by 2, 4 and 8; 16 x 2880 x 2880,
+    // 12 stages: 6.8 whole, 8.7 by 2).
+    const int stages = (a.k_tiles + 1) / 2;
+    for (int s = 8; s >= 2; s /= 2) {
+      if (max_blocks * n64 * s <= sms && stages - stages / s >= 12) {
+        f.mode = kSplit;
+        f.splits = s;
+        f.grid = static_cast<int>(max_blocks * n64 * s);
+        break;
+      }
+    }
+  }
+  f.b_rows = f.mode == kPair ? f.bn / 2 : f.bn;
+  return f;
+}
+
+cudaError_t launch_fp8b_gemm(const Fp8bArgs& a, const Fp8bForm& f, const Fp8bMaps& maps,
+                             cudaStream_t s) {
+  if (f.mode == kPair) return launch<128, kPair>(a, f, maps, s);
+  if (f.mode == kSplit) return launch<64, kSplit>(a, f, maps, s);
+  return f.bn == 128 ? launch<128, kSingle>(a, f, maps, s) : launch<64, kSingle>(a, f, maps, s);
 }
 
 }  // namespace moe

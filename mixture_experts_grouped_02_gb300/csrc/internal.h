@@ -240,6 +240,8 @@ struct Fp8bArgs {
   const int32_t* num_blocks;
   int max_blocks;              // entries of block_info, or ceil(M / 128)
   int subs;                    // 128-row parts of an align block
+  int block_m;                 // rows of an align block
+  int splits;                  // CTAs of a cluster that share a tile's K range
   long long cap;               // rows of a
   void* out;                   // (rows, N)
   int out_bf16, wide_out;      // wide_out: 16-byte stores fit every row
@@ -247,10 +249,21 @@ struct Fp8bArgs {
   unsigned long long timeout_ns;
   int starve;                  // failure-path test: the producer issues no copies
 };
-// tmA / tmAShort: a, boxes of 128 x 128 and 32 x 128 (rows x bytes); tmB: the
-// E * N weight rows, box of 256 x 128.
-cudaError_t launch_fp8b_gemm(Fp8bArgs a, const CUtensorMap& tmA, const CUtensorMap& tmAShort,
-                             const CUtensorMap& tmB, int sms, cudaStream_t s);
+// How a product is cut: weight rows of a tile, mode (gemm_fp8b.cu), CTAs that
+// share a tile's K range, CTAs in all, weight rows of a tensor-map box.
+struct Fp8bForm {
+  int bn, mode, splits, grid, b_rows;
+};
+Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, int pairs);
+// CTA pairs of the pair form the current device holds at once (0: unknown).
+int fp8b_max_pairs();
+// Tensor maps: a in boxes of 128 and 32 rows of 128 bytes; the E * N weight
+// rows in boxes of b_rows.
+struct Fp8bMaps {
+  CUtensorMap a, a_short, b;
+};
+cudaError_t launch_fp8b_gemm(const Fp8bArgs& a, const Fp8bForm& f, const Fp8bMaps& maps,
+                             cudaStream_t s);
 
 // Host helpers of moe_abi.cu: the current device's SM count, and the tensor
 // map of a row-major byte tensor (16-byte aligned, inner a multiple of 16)

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "internal.h"
@@ -42,8 +43,26 @@ int check_gemm(int E, int N, int K, int out_dtype) {
   return MOE_OK;
 }
 
+// Pairs the pair form holds at once on the current device, looked up once per
+// device.
+int pairs_held() {
+  static std::atomic<int> held[64];  // 0: not looked up; n + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  int v = held[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    v = fp8b_max_pairs() + 1;
+    held[dev].store(v, std::memory_order_relaxed);
+  }
+  return v - 1;
+}
+
+// `force`: null, or the form to use instead of fp8b_form's choice.
 int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int out_dtype,
-             cudaStream_t s) {
+             cudaStream_t s, const Fp8bForm* force = nullptr) {
   const int es = elem_bytes(out_dtype);
   if (!x || !a.a_scale || !w || !a.w_scale || !a.out || !aligned(x, 16) || !aligned(w, 16) ||
       !aligned(a.a_scale, 4) || !aligned(a.w_scale, 4) || !aligned(a.out, es))
@@ -53,13 +72,36 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
   a.cap = rows;
   a.out_bf16 = out_dtype == MOE_BF16;
   a.wide_out = (static_cast<long long>(a.N) * es) % 16 == 0 && aligned(a.out, 16);
-  a.timeout_ns = kWaitTimeoutNs;
-  CUtensorMap tmA, tmAShort, tmB;
-  int rc = make_byte_map(&tmA, x, a.K, rows, 128, 128);
-  if (rc == MOE_OK) rc = make_byte_map(&tmAShort, x, a.K, rows, 128, 32);
-  if (rc == MOE_OK) rc = make_byte_map(&tmB, w, a.K, static_cast<long long>(a.E) * a.N, 128, 256);
+  if (a.timeout_ns == 0) a.timeout_ns = kWaitTimeoutNs;
+  // tile indexes are 32-bit
+  if (static_cast<long long>(a.max_blocks) * a.subs * ((a.N + 63) / 64) > 0x3fffffffll)
+    return MOE_ERR_UNSUPPORTED;
+  const Fp8bForm f = force != nullptr ? *force : fp8b_form(a, device_sm_count(), pairs_held());
+  Fp8bMaps maps;
+  int rc = make_byte_map(&maps.a, x, a.K, rows, 128, 128);
+  if (rc == MOE_OK) rc = make_byte_map(&maps.a_short, x, a.K, rows, 128, 32);
+  if (rc == MOE_OK)
+    rc = make_byte_map(&maps.b, w, a.K, static_cast<long long>(a.E) * a.N, 128, f.b_rows);
   if (rc != MOE_OK) return rc;
-  return cuda_status(launch_fp8b_gemm(a, tmA, tmAShort, tmB, device_sm_count(), s));
+  return cuda_status(launch_fp8b_gemm(a, f, maps, s));
+}
+
+Fp8bArgs plain_args(const float* a_scale, const float* w_scale, int M, int N, int K, void* out,
+                    int32_t* status) {
+  Fp8bArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.E = 1;
+  g.max_blocks = M / 128 + (M % 128 != 0);
+  g.subs = 1;
+  g.block_m = 128;
+  g.a_scale = a_scale;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.status = status;
+  return g;
 }
 
 }  // namespace
@@ -136,19 +178,8 @@ int moe_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
   const int rc = check_gemm(1, N, K, out_dtype);
   if (rc != MOE_OK || M < 0) return rc != MOE_OK ? rc : MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  Fp8bArgs g;
-  std::memset(&g, 0, sizeof(g));
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  g.E = 1;
-  g.max_blocks = M / 128 + (M % 128 != 0);
-  g.subs = 1;
-  g.a_scale = a_scale;
-  g.w_scale = w_scale;
-  g.out = out;
-  g.status = dev_status;
-  return run_gemm(g, a, M, w, out_dtype, as_stream(stream));
+  return run_gemm(plain_args(a_scale, w_scale, M, N, K, out, dev_status), a, M, w, out_dtype,
+                  as_stream(stream));
 }
 
 int moe_grouped_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
@@ -171,11 +202,42 @@ int moe_grouped_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uin
   g.num_blocks = num_blocks;
   g.max_blocks = static_cast<int>(cap / block_m);
   g.subs = block_m > 128 ? block_m / 128 : 1;
+  g.block_m = block_m;
   g.a_scale = a_scale;
   g.w_scale = w_scale;
   g.out = out;
   g.status = dev_status;
   return run_gemm(g, a, static_cast<long long>(cap), w, out_dtype, as_stream(stream));
+}
+
+int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                            const float* w_scale, int M, int N, int K, void* out, int out_dtype,
+                            int form, unsigned long long wait_limit_ns, int32_t* dev_status,
+                            void* stream) {
+  const int rc = check_gemm(1, N, K, out_dtype);
+  if (rc != MOE_OK) return rc;
+  if (M <= 0 || form < 0 || form > 5) return MOE_ERR_INVALID_ARG;
+  if (wait_limit_ns != 0 && (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull))
+    return MOE_ERR_INVALID_ARG;
+  Fp8bArgs g = plain_args(a_scale, w_scale, M, N, K, out, dev_status);
+  g.timeout_ns = wait_limit_ns;
+  g.starve = wait_limit_ns != 0;
+  // {weight rows of a tile, mode, splits} of forms 0 to 5
+  static const int kForms[6][3] = {{64, 0, 1}, {128, 0, 1}, {128, 2, 1},
+                                   {64, 1, 2}, {64, 1, 4},  {64, 1, 8}};
+  Fp8bForm f;
+  f.bn = kForms[form][0];
+  f.mode = kForms[form][1];
+  f.splits = kForms[form][2];
+  f.b_rows = form == 2 ? 64 : f.bn;
+  const long long tiles = static_cast<long long>(form == 2 ? (g.max_blocks + 1) / 2 : g.max_blocks) *
+                          ((N + f.bn - 1) / f.bn);
+  if (tiles * f.splits > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
+  const int held = form == 2 ? pairs_held() : device_sm_count();
+  if (held <= 0) return MOE_ERR_CUDA;
+  f.grid = static_cast<int>(form >= 3 ? tiles * f.splits
+                                      : (form == 2 ? 2 : 1) * (tiles < held ? tiles : held));
+  return run_gemm(g, a, M, w, out_dtype, as_stream(stream), &f);
 }
 
 }  // extern "C"

@@ -158,6 +158,48 @@ def test_gemm(M, N, K, dtype):
     assert bool((guard[0] == 777).all()) and bool((guard[-1] == 777).all())
 
 
+@pytest.mark.parametrize("form", range(6))
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (5, 136, 400), (40, 200, 1168), (129, 520, 2064),
+                                   (300, 257, 640), (2100, 392, 144)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gemm_in_every_form(form, M, N, K, dtype):
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    guard = torch.full((M + 2, N), 777.0, dtype=dtype, device="cuda")
+    out = guard[1:-1]
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, moe.dtype_code(dtype), form)
+    _close(out, _dequant(a, sa), _dequant(w, sw, N), dtype)
+    assert bool((guard[0] == 777).all()) and bool((guard[-1] == 777).all())
+
+
+# sizes on the sides of the choice between the forms: pairs, one CTA of 128 and
+# of 64 weight rows, a split K
+@pytest.mark.parametrize("M,N,K", [(1300, 2000, 400), (100, 12800, 256), (2, 64, 7168),
+                                   (257, 576, 4096), (20000, 128, 272)])
+def test_gemm_across_the_choice_of_form(M, N, K):
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    got = moe.gemm_fp8_block(a, sa, w, sw)
+    _close(got, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
+
+
+@pytest.mark.parametrize("form", range(6))
+def test_waits_are_bounded(form):
+    """With no copies in flight every form's first wait runs out: it reports
+    MOE_ERR_TIMEOUT, writes nothing and leaves the device usable."""
+    M, N, K = 300, 400, 1024
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, 8), 3), _scales((4, 8), 4)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form, 2_000_000,
+                                 status)
+    assert moe.moe_get_device_status(status) == _abi.MOE_ERR_TIMEOUT
+    assert bool((out == 7).all())
+    got = moe.gemm_fp8_block(a, sa, w, sw)
+    _close(got, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
+
+
 def test_gemm_is_deterministic_and_takes_uint8():
     M, N, K = 48, 640, 1536 + 16
     a, w = _codes((M, K), 1), _codes((N, K), 2)
@@ -267,7 +309,8 @@ def _grouped(T, K, E, N, Kd, block_m, dtype, seed=0, skew=True, ids=None, base=0
     (1, 8, 256, 128, 256, 16), (1, 1, 1, 40, 16, 16), (8, 2, 8, 512, 1024, 16),
     (8, 8, 32, 264, 400, 16), (20, 4, 8, 300, 272, 32), (60, 2, 4, 520, 384, 64),
     (100, 3, 5, 256, 2080, 128), (300, 2, 8, 1000, 640, 128), (700, 2, 3, 260, 256, 256),
-    (513, 1, 2, 128, 128, 256)])
+    (513, 1, 2, 128, 128, 256), (3000, 2, 3, 1200, 400, 128), (2500, 1, 2, 2000, 272, 256),
+    (2000, 2, 2, 1000, 144, 64), (40, 2, 4, 64, 6400, 128)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_grouped(T, K, E, N, Kd, block_m, dtype):
     _grouped(T, K, E, N, Kd, block_m, dtype, seed=T)
