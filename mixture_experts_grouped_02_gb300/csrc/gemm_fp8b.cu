@@ -607,8 +607,6 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       const RowBlock r = block_of(t.mb);
       if (!live_tile(r)) continue;
       const int local = q * 32 + lane;
-      const long long row = r.r0 + local;
-      const bool row_ok = local < r.valid;
       const int col = t.nt * BN + col_in_tile;
       // warps without a row or a column of the output only keep the barriers
       const bool live = q * 32 < r.valid && col < a.N;
@@ -717,16 +715,12 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         }
       }
       if constexpr (MODE == kSplit) {
-        // partial sums, column-major, over the stages (all read by now)
-        float* part = reinterpret_cast<float*>(smem_gen) + col_in_tile * 128 + local;
-        if (live && row_ok) {
+        // partial sums over the stages (all read by now), a row's BN + 1
+        // floats apart so that neither side of the exchange meets a bank twice
+        float* part = reinterpret_cast<float*>(smem_gen) + local * (BN + 1) + col_in_tile;
+        if (live && local < r.valid) {
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) {
-            float lo, hi;
-            unpack2(acc[i], lo, hi);
-            part[(2 * i) * 128] = lo;
-            part[(2 * i + 1) * 128] = hi;
-          }
+          for (int i = 0; i < C::kCols / 2; ++i) unpack2(acc[i], part[2 * i], part[2 * i + 1]);
         }
       } else {
         if (live && !s_abort)
@@ -754,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         float sum = 0.0f;
         for (int p = 0; p < a.splits; ++p)
           sum += __uint_as_float(
-              ld_shared_cluster_u32(mapa_shared(smemA, p) + 4u * (c * 128 + m)));
+              ld_shared_cluster_u32(mapa_shared(smemA, p) + 4u * (m * (BN + 1) + c)));
         const long long o = static_cast<long long>(r.r0 + m) * a.N + col;
         if (a.out_bf16)
           static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(sum);
@@ -807,24 +801,31 @@ cudaError_t launch(Fp8bArgs a, const Fp8bForm& f, const Fp8bMaps& maps, cudaStre
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }
 
-}  // namespace
-
-// CTA pairs of the pair form the current device holds at once, 0 if unknown.
-int fp8b_max_pairs() {
-  using C = Cfg<128, kPair>;
-  if (prepare_kernel<128, kPair>() != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
+// Clusters of `ctas` CTAs of the split form (4 and 8) or CTA pairs of the pair
+// form (2) the current device holds at once, 0 if unknown.
+template <int BN, int MODE>
+int max_clusters(int ctas) {
+  using C = Cfg<BN, MODE>;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(2), dim3(C::kThreads), C::kSmemBytes, nullptr, attr, 2);
+      pdl_config(dim3(ctas), dim3(C::kThreads), C::kSmemBytes, nullptr, attr, ctas);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fp8b_gemm_kernel<128, kPair>, &cfg) != cudaSuccess) {
+  if (prepare_kernel<BN, MODE>() != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fp8b_gemm_kernel<BN, MODE>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   return n;
+}
+}  // namespace
+
+Fp8bHeld fp8b_held() {
+  Fp8bHeld h;
+  h.pairs = max_clusters<128, kPair>(2);
+  h.split[0] = max_clusters<64, kSplit>(2);
+  h.split[1] = max_clusters<64, kSplit>(4);
+  h.split[2] = max_clusters<64, kSplit>(8);
+  return h;
 }
 
 // The form with the least estimated time: rounds of tiles times what a stage
@@ -836,8 +837,9 @@ int fp8b_max_pairs() {
 // list's row blocks are estimated from its capacity: at least one row per
 // align block and all but the padding of E blocks; half a block of padding per
 // expert that has rows.
-Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, int pairs) {
+Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
   Fp8bForm f;
+  const int pairs = held.pairs;
   f.splits = 1;
   const long long n64 = div_up(a.N, 64), n128 = div_up(a.N, 128);
   const long long max_blocks = static_cast<long long>(a.max_blocks) * a.subs;
@@ -870,17 +872,21 @@ Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, int pairs) {
     f.bn = 64;
     f.mode = kSingle;
     f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n64));
-    // Splitting K costs about 3.5 us of cluster launch, barriers and joining:
-    // for one round of tiles with at least 12 stages fewer per CTA (1 x 576 x
-    // 7168: 11.2 us whole, 9.3, 7.4 and 6.8 by 2, 4 and 8; 16 x 2880 x 2880,
-    // 12 stages: 6.8 whole, 8.7 by 2).
+    // Splitting K by s, where all the clusters are resident at once: 0.29 us
+    // for every stage a CTA has less, against 2.5 us of cluster launch,
+    // barriers and joining and 0.06 us per row a CTA joins (1 x 576 x 7168:
+    // 11.2 us whole, 9.3, 7.4 and 6.8 by 2, 4 and 8; 16 x 2880 x 2880: 6.9
+    // whole, 8.5 by 2; 128 x 4096 x 7168: 13.3 whole, 15.4 by 2).
     const int stages = (a.k_tiles + 1) / 2;
-    for (int s = 8; s >= 2; s /= 2) {
-      if (max_blocks * n64 * s <= sms && stages - stages / s >= 12) {
+    const double rows = a.block_info != nullptr ? std::min(a.block_m, 128) : std::min(a.M, 128);
+    double best = 0.0;
+    for (int i = 0, s = 2; i < 3; ++i, s *= 2) {
+      const double gain = 0.29 * (stages - div_up(stages, s)) - 2.5 - 0.06 * rows / s;
+      if (max_blocks * n64 <= held.split[i] && gain > best) {
+        best = gain;
         f.mode = kSplit;
         f.splits = s;
         f.grid = static_cast<int>(max_blocks * n64 * s);
-        break;
       }
     }
   }

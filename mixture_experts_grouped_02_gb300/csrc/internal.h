@@ -254,9 +254,13 @@ struct Fp8bArgs {
 struct Fp8bForm {
   int bn, mode, splits, grid, b_rows;
 };
-Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, int pairs);
-// CTA pairs of the pair form the current device holds at once (0: unknown).
-int fp8b_max_pairs();
+// CTA pairs, and clusters of 2, 4 and 8 CTAs of the split form, the current
+// device holds at once (0: unknown).
+struct Fp8bHeld {
+  int pairs, split[3];
+};
+Fp8bHeld fp8b_held();
+Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held);
 // Tensor maps: a in boxes of 128 and 32 rows of 128 bytes; the E * N weight
 // rows in boxes of b_rows.
 struct Fp8bMaps {

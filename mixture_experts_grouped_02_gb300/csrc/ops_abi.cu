@@ -3,8 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstring>
+#include <mutex>
 
 #include "internal.h"
 
@@ -43,21 +43,23 @@ int check_gemm(int E, int N, int K, int out_dtype) {
   return MOE_OK;
 }
 
-// Pairs the pair form holds at once on the current device, looked up once per
-// device.
-int pairs_held() {
-  static std::atomic<int> held[64];  // 0: not looked up; n + 1
+// What the product's forms hold at once on the current device, looked up once
+// per device.
+Fp8bHeld held_clusters() {
+  static std::mutex mu;
+  static bool known[64];
+  static Fp8bHeld held[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
-    return 0;
+    return Fp8bHeld{};
   }
-  int v = held[dev].load(std::memory_order_relaxed);
-  if (v == 0) {
-    v = fp8b_max_pairs() + 1;
-    held[dev].store(v, std::memory_order_relaxed);
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[dev]) {
+    held[dev] = fp8b_held();
+    known[dev] = true;
   }
-  return v - 1;
+  return held[dev];
 }
 
 // `force`: null, or the form to use instead of fp8b_form's choice.
@@ -76,7 +78,7 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
   // tile indexes are 32-bit
   if (static_cast<long long>(a.max_blocks) * a.subs * ((a.N + 63) / 64) > 0x3fffffffll)
     return MOE_ERR_UNSUPPORTED;
-  const Fp8bForm f = force != nullptr ? *force : fp8b_form(a, device_sm_count(), pairs_held());
+  const Fp8bForm f = force != nullptr ? *force : fp8b_form(a, device_sm_count(), held_clusters());
   Fp8bMaps maps;
   int rc = make_byte_map(&maps.a, x, a.K, rows, 128, 128);
   if (rc == MOE_OK) rc = make_byte_map(&maps.a_short, x, a.K, rows, 128, 32);
@@ -233,7 +235,7 @@ int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_
   const long long tiles = static_cast<long long>(form == 2 ? (g.max_blocks + 1) / 2 : g.max_blocks) *
                           ((N + f.bn - 1) / f.bn);
   if (tiles * f.splits > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
-  const int held = form == 2 ? pairs_held() : device_sm_count();
+  const int held = form == 2 ? held_clusters().pairs : device_sm_count();
   if (held <= 0) return MOE_ERR_CUDA;
   f.grid = static_cast<int>(form >= 3 ? tiles * f.splits
                                       : (form == 2 ? 2 : 1) * (tiles < held ? tiles : held));
