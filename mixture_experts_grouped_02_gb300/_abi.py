@@ -190,9 +190,7 @@ def status_string(status: int) -> str:
 
 
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or type(t) is int:
         return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
@@ -204,12 +202,13 @@ def _p(t):
 # (device) -> the current stream's handle: what current_stream().cuda_stream
 # gives, without building a Stream object (0.1 us instead of 2.9)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -169,6 +169,8 @@ int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, 
   const int es = elem_bytes(x_dtype);
   if (T < 0 || H <= 0 || es == 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
+  // blocks are counted in 32 bits, and so are their CTAs
+  if (static_cast<long long>(T) * ((H + 127ll) / 128) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
   if (!x || !xq || !scale || !aligned(x, es)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       launch_quantize_block(x, x_dtype, T, H, gated, xq, scale, as_stream(stream)));

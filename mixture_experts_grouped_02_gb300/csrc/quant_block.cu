@@ -13,8 +13,11 @@
 //
 // Gated: v = gate / (1 + e^-gate) * up, the row holding gate then up.
 //
-// One pass: 16 lanes own a block, 8 columns each, kept in registers between
-// the maximum and the codes.  Bound by HBM.
+// One pass: a team of lanes owns a block and keeps it in registers between
+// the maximum and the codes.  Bound by HBM for fp32, and for bf16, half the
+// bytes for the same arithmetic, close to its instructions: teams of 8 lanes
+// with 16 columns each there (two loads and one store of 16 bytes, one
+// division per 16 columns), 16 lanes with 8 columns otherwise.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -26,45 +29,51 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLanes = 16;                       // lanes of a block
-constexpr int kCols = 8;                         // columns of a lane
-constexpr int kBlock = kLanes * kCols;           // 128
-constexpr int kTeams = kThreads / kLanes;
+constexpr int kBlock = 128;
 constexpr float kAmaxFloor = 7.8886090522101181e-31f;  // 2^-100
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-// Columns of this lane: 8 consecutive ones (WIDE, 16-byte loads), or every
-// 16th one with a bounds check.
-template <typename T, bool WIDE>
+// Columns of a lane: COLS consecutive ones (WIDE, 16-byte loads; rows end on a
+// multiple of COLS), or every (128 / COLS)th one with a bounds check.
+template <typename T, bool WIDE, int COLS>
 __device__ __forceinline__ void load_cols(const T* __restrict__ row, int c0, int lane, int H,
-                                          float (&v)[kCols]) {
+                                          float (&v)[COLS]) {
   if constexpr (!WIDE) {
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const int c = c0 + lane + kLanes * i;
+    for (int i = 0; i < COLS; ++i) {
+      const int c = c0 + lane + kBlock / COLS * i;
       v[i] = c < H ? static_cast<float>(row[c]) : 0.0f;
     }
   } else {
-    const int c = c0 + kCols * lane;
-    if (c >= H) {  // H is a multiple of 8
+    const int c = c0 + COLS * lane;
+    if (c >= H) {
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
+      for (int i = 0; i < COLS; ++i) v[i] = 0.0f;
     } else if constexpr (sizeof(T) == 2) {
-      const uint4 q = *reinterpret_cast<const uint4*>(row + c);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint4 q[COLS / 8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int h = 0; h < COLS / 8; ++h) q[h] = reinterpret_cast<const uint4*>(row + c)[h];
+#pragma unroll
+      for (int h = 0; h < COLS / 8; ++h) {
+        const uint32_t w[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
+          v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
       }
     } else {
-      const float4 p = reinterpret_cast<const float4*>(row + c)[0];
-      const float4 q = reinterpret_cast<const float4*>(row + c)[1];
-      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
-      v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+#pragma unroll
+      for (int h = 0; h < COLS / 4; ++h) {
+        const float4 p = reinterpret_cast<const float4*>(row + c)[h];
+        v[4 * h] = p.x;
+        v[4 * h + 1] = p.y;
+        v[4 * h + 2] = p.z;
+        v[4 * h + 3] = p.w;
+      }
     }
   }
 }
@@ -75,67 +84,81 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return h;
 }
 
-template <typename T, bool GATED, bool WIDE>
+template <typename T, bool GATED, bool WIDE, int COLS>
 __global__ void __launch_bounds__(kThreads)
-    quantize_block_kernel(const T* __restrict__ x, long long blocks, int H, int nb,
+    quantize_block_kernel(const T* __restrict__ x, unsigned blocks, int H, unsigned nb,
                           uint8_t* __restrict__ xq, float* __restrict__ scale) {
+  constexpr int LANES = kBlock / COLS;
+  constexpr unsigned kTeams = kThreads / LANES;
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & (kLanes - 1);
-  const unsigned half = 0xffffu << (threadIdx.x & 16);
-  for (long long j = static_cast<long long>(blockIdx.x) * kTeams + threadIdx.x / kLanes;
-       j < blocks; j += static_cast<long long>(gridDim.x) * kTeams) {
-    const long long t = j / nb;
-    const int c0 = static_cast<int>(j - t * nb) * kBlock;
-    const T* row = x + t * (GATED ? 2ll * H : H);
-    float v[kCols];
-    load_cols<T, WIDE>(row, c0, lane, H, v);
-    if constexpr (GATED) {
-      float u[kCols];
-      load_cols<T, WIDE>(row + H, c0, lane, H, u);
+  const int lane = threadIdx.x & (LANES - 1);
+  const unsigned team = ((1u << LANES) - 1u) << (threadIdx.x & (32 - LANES));
+  const unsigned j = blockIdx.x * kTeams + threadIdx.x / LANES;
+  if (j >= blocks) return;
+  const unsigned t = j / nb;
+  const int c0 = static_cast<int>(j - t * nb) * kBlock;
+  const T* row = x + static_cast<long long>(t) * (GATED ? 2ll * H : H);
+  float v[COLS];
+  load_cols<T, WIDE, COLS>(row, c0, lane, H, v);
+  if constexpr (GATED) {
+    float u[COLS];
+    load_cols<T, WIDE, COLS>(row + H, c0, lane, H, u);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] = silu_mul(v[i], u[i]);
+    for (int i = 0; i < COLS; ++i) v[i] = silu_mul(v[i], u[i]);
+  }
+  float m = kAmaxFloor;
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+  for (int d = LANES / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(team, m, d));
+  const float r = __fdiv_rn(448.0f, m);
+  if (lane == 0) scale[j] = __fdiv_rn(m, 448.0f);
+  uint8_t* q = xq + static_cast<long long>(t) * H;
+  if constexpr (WIDE) {
+    if (c0 + COLS * lane < H) {
+      uint32_t p[COLS / 4];
+#pragma unroll
+      for (int i = 0; i < COLS / 4; ++i)
+        p[i] = e4m3x2(v[4 * i] * r, v[4 * i + 1] * r) |
+               (e4m3x2(v[4 * i + 2] * r, v[4 * i + 3] * r) << 16);
+      if constexpr (COLS == 16)
+        *reinterpret_cast<uint4*>(q + c0 + COLS * lane) = make_uint4(p[0], p[1], p[2], p[3]);
+      else
+        *reinterpret_cast<uint2*>(q + c0 + COLS * lane) = make_uint2(p[0], p[1]);
     }
-    float m = kAmaxFloor;
+  } else {
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, d));
-    const float r = __fdiv_rn(448.0f, m);
-    if (lane == 0) scale[j] = __fdiv_rn(m, 448.0f);
-    uint8_t* q = xq + t * H;
-    if constexpr (WIDE) {
-      if (c0 + kCols * lane < H) {
-        const uint32_t a = e4m3x2(v[0] * r, v[1] * r) | (e4m3x2(v[2] * r, v[3] * r) << 16);
-        const uint32_t b = e4m3x2(v[4] * r, v[5] * r) | (e4m3x2(v[6] * r, v[7] * r) << 16);
-        *reinterpret_cast<uint2*>(q + c0 + kCols * lane) = make_uint2(a, b);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const int c = c0 + lane + kLanes * i;
-        if (c < H) q[c] = static_cast<uint8_t>(e4m3x2(v[i] * r, 0.0f));
-      }
+    for (int i = 0; i < COLS; ++i) {
+      const int c = c0 + lane + LANES * i;
+      if (c < H) q[c] = static_cast<uint8_t>(e4m3x2(v[i] * r, 0.0f));
     }
   }
 }
 
-template <typename T, bool GATED>
-cudaError_t launch_as(const void* x, int T_, int H, uint8_t* xq, float* scale, cudaStream_t s) {
-  const int nb = (H + kBlock - 1) / kBlock;
-  const long long blocks = static_cast<long long>(T_) * nb;
-  const unsigned grid = static_cast<unsigned>(
-      std::min<long long>((blocks + kTeams - 1) / kTeams, 0x7fffffffll));
+template <typename T, bool GATED, bool WIDE, int COLS>
+cudaError_t launch_cols(const T* x, int rows, int H, uint8_t* xq, float* scale, cudaStream_t s) {
+  const unsigned nb = static_cast<unsigned>((H + kBlock - 1) / kBlock);
+  const unsigned blocks = static_cast<unsigned>(rows) * nb;  // the caller checks that it fits
+  const unsigned teams = kThreads / (kBlock / COLS);
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(kThreads), 0, s, attr);
-  const bool wide = H % kCols == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
-                    (reinterpret_cast<uintptr_t>(xq) & 7u) == 0;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(dim3(blocks / teams + (blocks % teams != 0)), dim3(kThreads), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, quantize_block_kernel<T, GATED, WIDE, COLS>, x, blocks, H, nb,
+                            xq, scale);
+}
+
+template <typename T, bool GATED>
+cudaError_t launch_as(const void* x, int rows, int H, uint8_t* xq, float* scale, cudaStream_t s) {
+  auto aligned = [&](int cols, unsigned out) {
+    return H % cols == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
+           (reinterpret_cast<uintptr_t>(xq) & (out - 1)) == 0;
+  };
   const T* xt = static_cast<const T*>(x);
-  if (wide)
-    return cudaLaunchKernelEx(&cfg, quantize_block_kernel<T, GATED, true>, xt, blocks, H, nb, xq,
-                              scale);
-  return cudaLaunchKernelEx(&cfg, quantize_block_kernel<T, GATED, false>, xt, blocks, H, nb, xq,
-                            scale);
+  if (sizeof(T) == 2 && aligned(16, 16))
+    return launch_cols<T, GATED, true, 16>(xt, rows, H, xq, scale, s);
+  if (aligned(8, 8)) return launch_cols<T, GATED, true, 8>(xt, rows, H, xq, scale, s);
+  return launch_cols<T, GATED, false, 8>(xt, rows, H, xq, scale, s);
 }
 
 }  // namespace

@@ -18,22 +18,25 @@ def _nblk(n):
     return (n + 127) // 128
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _codes(t, shape, what):
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t.dtype not in _CODES:
         raise ValueError(f"{what}: expected e4m3 codes, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
 
 
 def _scales(t, shape, what):
-    if t.dtype != torch.float32 or tuple(t.shape) != shape:
+    if t.dtype != torch.float32 or t.shape != shape:
         raise ValueError(f"{what}: expected float32 {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _result(out, rows, N, dtype, device, stream):
     if out is None:
         out = _empty((rows, N), dtype, device, stream)
-    elif out.dim() != 2 or out.shape[0] != rows or out.shape[1] != N:
+    elif out.shape != (rows, N):
         raise ValueError(f"out: expected shape ({rows}, {N}), got {tuple(out.shape)}")
     return out, _dtype(out, _ROWS)
 
@@ -81,7 +84,7 @@ def grouped_gemm_fp8_block(a, a_scale, w, w_scale, plan, block_m=128, out=None,
     E, N = w.shape[0], w.shape[1]
     cap = _lists(plan)[2]
     info, num = plan["block_info"], plan["num_blocks"]
-    if block_m <= 0 or tuple(info.shape) != (cap // block_m, 4):
+    if block_m <= 0 or info.shape != (cap // block_m, 4):
         raise ValueError(f"block_info {tuple(info.shape)} does not fit {cap} slots in blocks of "
                          f"{block_m}")
     if info.dtype != torch.int32 or num.dtype != torch.int32:

@@ -33,7 +33,7 @@ def _lists(plan):
 
 
 def _rows(t, rows, H, dtype, what):
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != H or t.dtype != dtype:
+    if t.shape != (rows, H) or t.dtype != dtype:
         raise ValueError(f"{what}: expected a ({rows}, {H}) {dtype} tensor, got "
                          f"{tuple(t.shape)} {t.dtype}")
     return t
@@ -50,6 +50,8 @@ def _on(stream):
 
 
 def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with _on(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
