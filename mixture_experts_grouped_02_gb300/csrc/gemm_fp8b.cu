@@ -15,10 +15,9 @@
 // Three forms of one kernel, a template over the weight rows BN of a tile and
 // the mode (fp8b_form chooses, with what each measured):
 //  * kPair: a CTA pair computes 256 rows x 128 weight rows with cta_group::2
-//    MMAs, each CTA holding 128 rows of a and half of the weight rows.  What
-//    an MMA takes is set by the operand bytes it reads from shared memory,
-//    about 75 per clock: M = 128, N = 128 takes 133 clocks on one CTA and 83
-//    as a pair, where each CTA reads half of the weight rows;
+//    MMAs, each CTA holding 128 rows of a and half of the weight rows: 96 KB
+//    through shared memory (copies in, operand reads out) per two scale
+//    blocks where one CTA with a 128 x 128 tile of its own moves 128 KB;
 //  * kSingle: one CTA per tile of 128 rows x BN, for lists of small blocks
 //    (weight streaming) and products with too few rows for pairs;
 //  * kSplit: a cluster of 2 to 8 CTAs shares one tile's K range and adds the
@@ -41,10 +40,13 @@
 //    3-10 epilogue: warp w reads the lane quarter w % 4 and one half of the
 //    columns.  A warp whose 32 rows are all padding only keeps the barriers.
 //
-// 8192 x 4096 x 7168: 202-213 us, 2.3 PFLOP/s.  A stage takes a pair about 790
-// clocks, of which the MMAs are 660; what is left is the chain from the last
-// MMA of a buffer over its epilogue to the next MMA into it (240 + 590 + 225
-// clocks beside the MMAs, over two buffers, all that TMEM holds).
+// 8192 x 4096 x 7168 (at 1.9 GHz): 199-213 us as pairs, 2.3-2.4 PFLOP/s, 217
+// with 128 and 272 with 64 weight rows to a CTA.  Two scale blocks take a pair
+// about 790 clocks, 512 of them MMAs at the full rate: the rest is the chain
+// from the last MMA of a buffer over its epilogue to the next MMA into it
+// (240 + 590 + 225 clocks beside the MMAs, over two buffers, which fill
+// TMEM).  One CTA takes 820 for 128 weight rows, which its MMA thread is
+// never kept waiting for: 128 KB through shared memory.
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
 // up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
@@ -85,7 +87,16 @@ struct Cfg {
   static constexpr int kBufs = 2;
   static constexpr int kBufCols = kSub * BN_;
   static constexpr int kTmemCols = kBufs * kBufCols;
-  static_assert(kStages > kBufs, "the scale slots need a stage more than buffers");
+  // Scale slots.  Stage j takes the slot of stage j - kSlots, free once the MMAs
+  // of stage i = j - kSlots + kBufs are done, and waits for those on the
+  // barrier of i's stage, which must not be a round ahead by then: the MMAs
+  // have come to stage j - 1 (they wait for the scales of j), or in a pair,
+  // where only the epilogue waits for them, to j + 1.  (With kStages slots
+  // everywhere, one CTA of 128 weight rows could write the scales of a stage
+  // only after the MMAs of the stage before it: 249 us instead of 217 for 8192
+  // x 4096 x 7168.)
+  static constexpr int kSlots = MODE == kPair ? kStages : kStages + kBufs;
+  static_assert(kStages > kBufs && kSlots <= kStages + kBufs, "see above");
   static constexpr int kMmaWarp = 1;
   static constexpr int kScaleWarp = 2;
   static constexpr int kFirstEpi = 3;
@@ -312,8 +323,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[C::kStages];
   __shared__ __align__(8) uint64_t acce_bar[C::kBufs];
   __shared__ __align__(8) uint64_t scale_bar[C::kStages];
-  // sa * sb of the tile's rows for the scale blocks of each stage
-  __shared__ float s_scale[C::kStages][C::kSub][128];
+  // sa * sb of the tile's rows for the scale blocks of a stage
+  __shared__ float s_scale[C::kSlots][C::kSub][128];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_skip;
@@ -531,14 +542,20 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       }
     } else if (warp == C::kScaleWarp && !a.starve) {
       // ----------------------------------------------------- scales
-      // A lane has four rows; a stage's scale blocks are loaded while those
-      // of the stage before it are written.  Stage j takes the slot of stage
-      // j - kStages, which the epilogue has read once the MMAs of stage
-      // j - kStages + kBufs are done (they wait for its buffer).
-      uint32_t stage = 0;
-      int w_stage = C::kBufs % C::kStages;  // of stage j - kStages + kBufs
+      // A lane has four rows; the scale blocks of kGroup stages are loaded
+      // together (a 32-byte sector of each row), while those of the kGroup
+      // stages before them are written.  The epilogue has read the slot of
+      // stage j - kSlots once the MMAs of stage j - kSlots + kBufs are done,
+      // as they wait for its buffer.
+      constexpr int kGroup = 4, kBlocks = kGroup * C::kSub;
+      uint32_t stage = 0, slot = 0;
+      // The first kStages stages wait for nothing.  From then on stage j
+      // waits for the MMAs of j - kSlots + kBufs, in one CTA those of
+      // j - kStages: its arrival below must not come before the phase of the
+      // full barrier it counts in.
+      int w_stage = C::kStages - C::kSlots + C::kBufs;
       uint32_t w_phase = 0;
-      int fresh = C::kStages;  // slots not used before
+      int fresh = C::kStages;
       bool ok = true;
       for (int tile = first; tile < total && ok; tile += step) {
         const Tile t = decode_tile(tile, num_blocks, a);
@@ -548,10 +565,10 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
                                        t.nt * BN / 128) * a.k_tiles;
         const float* sa = a.a_scale + (static_cast<long long>(r.r0) + lane) * a.k_tiles;
         const long long row32 = 32ll * a.k_tiles;
-        float na[C::kSub][4], nb[C::kSub];
+        float na[kBlocks][4], nb[kBlocks];
         auto load = [&](int kt) {
 #pragma unroll
-          for (int u = 0; u < C::kSub; ++u) {
+          for (int u = 0; u < kBlocks; ++u) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               na[u][i] = kt + u < ke && lane + 32 * i < r.valid ? __ldg(sa + i * row32 + kt + u)
@@ -560,37 +577,43 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           }
         };
         load(kb);
-        for (int kt = kb; kt < ke; kt += C::kSub) {
-          float s[C::kSub][4];
+        for (int k0 = kb; k0 < ke && ok; k0 += kBlocks) {
+          float s[kBlocks][4];
 #pragma unroll
-          for (int u = 0; u < C::kSub; ++u)
+          for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[u][i] = na[u][i] * nb[u];
-          load(kt + C::kSub);
-          if (fresh > 0) {
-            --fresh;
-          } else {
-            const int good =
-                mbar_wait_suspend(smem_u32(&empty_bar[w_stage]), w_phase, &s_abort, to);
-            if (!__all_sync(0xffffffffu, good)) {
-              ok = false;
-              break;
+          load(k0 + kBlocks);
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) {
+            if (k0 + g * C::kSub >= ke || !ok) break;
+            if (fresh > 0) {
+              --fresh;
+            } else {
+              const int good =
+                  mbar_wait_suspend(smem_u32(&empty_bar[w_stage]), w_phase, &s_abort, to);
+              if (!__all_sync(0xffffffffu, good)) {
+                ok = false;
+                break;
+              }
+              if (++w_stage == C::kStages) {
+                w_stage = 0;
+                w_phase ^= 1;
+              }
             }
-            if (++w_stage == C::kStages) {
-              w_stage = 0;
-              w_phase ^= 1;
-            }
+#pragma unroll
+            for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                s_scale[slot][u][32 * i + lane] = s[g * C::kSub + u][i];
+            // One CTA: the slot joins its stage's full barrier, and whoever
+            // sees that stage's MMAs done sees it too.  A pair's full barrier
+            // is the leader's alone: a barrier of its own.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(PAIR ? &scale_bar[stage] : &full_bar[stage]));
+            if (++stage == C::kStages) stage = 0;
+            if (++slot == C::kSlots) slot = 0;
           }
-#pragma unroll
-          for (int u = 0; u < C::kSub; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s_scale[stage][u][32 * i + lane] = s[u][i];
-          // One CTA: the slot joins its stage's full barrier, and whoever
-          // sees that stage's MMAs done sees it too.  A pair's full barrier
-          // is the leader's alone: a barrier of its own.
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(PAIR ? &scale_bar[stage] : &full_bar[stage]));
-          if (++stage == C::kStages) stage = 0;
         }
       }
     }
@@ -601,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
     const int col_in_tile = ((warp - C::kFirstEpi) >> 2) * C::kCols;
     const uint32_t acce0 =
         PAIR ? mapa_shared(smem_u32(&acce_bar[0]), 0) : smem_u32(&acce_bar[0]);
-    uint32_t buf = 0, stage = 0, phase = 0;
+    uint32_t buf = 0, stage = 0, phase = 0, slot = 0;
     for (int tile = first; tile < total; tile += step) {
       const Tile t = decode_tile(tile, num_blocks, a);
       const RowBlock r = block_of(t.mb);
@@ -636,6 +659,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       };
       auto next_stage = [&] {
         buf ^= 1;
+        if (++slot == C::kSlots) slot = 0;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1;
@@ -661,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
                     v);
         };
         auto scale = [&](int u) {
-          const uint32_t s = __float_as_uint(s_scale[stage][u][local]);
+          const uint32_t s = __float_as_uint(s_scale[slot][u][local]);
           s2 = pack2(s, s);
         };
         auto add = [&](int j, const uint32_t(&v)[32]) {
@@ -829,14 +853,14 @@ Fp8bHeld fp8b_held() {
 }
 
 // The form with the least estimated time: rounds of tiles times what a stage
-// takes (GB300, us: 0.40 with 64 weight rows, 0.59 with 128, 0.52 for a pair;
-// 8192 x 4096 x 7168 took 305, 232 and 202).  Measured around the choice:
-// 333 x 2880 x 2880 in 8.4 us with 64 rows, 12 with 128 and 13 as pairs; 1024 x
-// 4096 x 7168 in 47, 36 and 34; 8192 rows of 32 experts against 4096 x 7168 in
-// 407, 300 and 344 (a pair's second half is often padding there).  A sorted
-// list's row blocks are estimated from its capacity: at least one row per
-// align block and all but the padding of E blocks; half a block of padding per
-// expert that has rows.
+// takes (GB300, us: 0.36 with 64 weight rows, 0.55 with 128, 0.53 for a pair;
+// 8192 x 4096 x 7168 took 272, 217 and 208).  Measured around the choice:
+// 333 x 2880 x 2880 in 8.2 us with 64 rows, 9.8 with 128 and 11.6 as pairs;
+// 1024 x 4096 x 7168 in 43, 33.4 and 33.8; 8192 rows of 32 experts against 4096
+// x 7168 in 407, 296 and 344 (a pair's second half is often padding there).  A
+// sorted list's row blocks are estimated from its capacity: at least one row
+// per align block and all but the padding of E blocks; half a block of padding
+// per expert that has rows.
 Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
   Fp8bForm f;
   const int pairs = held.pairs;
@@ -855,9 +879,9 @@ Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
     two = a.block_m < 128 ? blocks : std::min(blocks, rows / 256.0 + experts / 2);
   }
   auto rounds = [](double tiles, int at_once) { return std::ceil(tiles / at_once); };
-  const double us64 = 0.40 * rounds(blocks * n64, sms);
-  const double us128 = 0.59 * rounds(blocks * n128, sms);
-  const double us_pair = can_pair ? 0.52 * rounds(two * n128, pairs) : 1e30;
+  const double us64 = 0.36 * rounds(blocks * n64, sms);
+  const double us128 = 0.55 * rounds(blocks * n128, sms);
+  const double us_pair = can_pair ? 0.53 * rounds(two * n128, pairs) : 1e30;
   const long long pair_tiles =
       (a.block_info != nullptr && a.subs == 1 ? max_blocks : div_up(max_blocks, 2)) * n128;
   if (us_pair <= us64 && us_pair <= us128) {
