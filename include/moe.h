@@ -553,9 +553,8 @@ int moe_test_gemm_wait_timeout(const moe_problem_t* p, int gemm, const void* a_r
                                int32_t* dev_status, void* stream);
 
 /* moe_gemm_fp8_block (M >= 1) in a given form of its kernel (gemm_fp8b.cu): 0
- * and 1 one CTA per tile of 64 and 128 weight rows, 2 CTA pairs, 3 to 5 the K
- * range split over clusters of 2, 4 and 8 CTAs; moe_gemm_fp8_block chooses by
- * the sizes.  wait_limit_ns 0 computes the product; 1 ms to 2 s runs the
+ * and 1 one CTA per tile of 64 and 128 weight rows, 2 to 4 the K range split
+ * over clusters of 2, 4 and 8 CTAs; moe_gemm_fp8_block chooses by the sizes.  wait_limit_ns 0 computes the product; 1 ms to 2 s runs the
  * failure path as above (no copies, MOE_ERR_TIMEOUT in *dev_status, out not
  * written).  For tests. */
 int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,

@@ -12,14 +12,9 @@
 // MMA's M side), and the columns of a thread have one weight scale, so this
 // costs one packed fma.rn.f32x2 for two elements.
 //
-// Three forms of one kernel, a template over the weight rows BN of a tile and
+// Two forms of one kernel, a template over the weight rows BN of a tile and
 // the mode (fp8b_form chooses, with what each measured):
-//  * kPair: a CTA pair computes 256 rows x 128 weight rows with cta_group::2
-//    MMAs, each CTA holding 128 rows of a and half of the weight rows: 96 KB
-//    through shared memory (copies in, operand reads out) per two scale
-//    blocks where one CTA with a 128 x 128 tile of its own moves 128 KB;
-//  * kSingle: one CTA per tile of 128 rows x BN, for lists of small blocks
-//    (weight streaming) and products with too few rows for pairs;
+//  * kSingle: one CTA per tile of 128 rows x BN weight rows, 128 or 64;
 //  * kSplit: a cluster of 2 to 8 CTAs shares one tile's K range and adds the
 //    partial sums through distributed shared memory, in rank order, for
 //    products with fewer tiles than SMs and a long K.
@@ -27,26 +22,28 @@
 // Layout per CTA (one per SM, persistent, tiles walked in bands as in
 // sched.cuh; kSplit: one tile per cluster):
 //  * 192 KB of stages of two scale blocks each: A 2 x 128 rows x 128 bytes (32
-//    rows when the row block has at most 32 valid rows), B 2 x BN (kPair:
-//    BN / 2) rows, 128-byte swizzled, by TMA.  K past the tensor reads as
-//    zero codes.  Two blocks to a stage because a handshake costs about as
-//    much as a block's MMAs: a look at an mbarrier 55 clocks and more under
-//    load, a commit until its waiters run 240;
+//    rows when the row block has at most 32 valid rows), B 2 x BN rows,
+//    128-byte swizzled, by TMA.  K past the tensor reads as zero codes.  Two
+//    blocks to a stage because a handshake costs about as much as a block's
+//    MMAs: a look at an mbarrier 55 clocks and more under load, a commit until
+//    its waiters run 240;
 //  * TMEM: two buffers of two fp32 blocks of BN columns; the columns past N
 //    in the last tile are left out of the MMA's N;
 //  * warp 0 TMA, warp 1 MMA, warp 2 the row scales (loaded by the threads
 //    that need them they took 32 L1 lines per load and warp and held up the
-//    buffers' release, 285 us instead of 218 for 8192 x 4096 x 7168), warps
-//    3-10 epilogue: warp w reads the lane quarter w % 4 and one half of the
-//    columns.  A warp whose 32 rows are all padding only keeps the barriers.
+//    buffers' release), warps 3-10 epilogue: warp w reads the lane quarter w %
+//    4 and one half of the columns.  A warp whose 32 rows are all padding only
+//    keeps the barriers.
 //
-// 8192 x 4096 x 7168 (at 1.9 GHz): 199-213 us as pairs, 2.3-2.4 PFLOP/s, 217
-// with 128 and 272 with 64 weight rows to a CTA.  Two scale blocks take a pair
-// about 790 clocks, 512 of them MMAs at the full rate: the rest is the chain
-// from the last MMA of a buffer over its epilogue to the next MMA into it
-// (240 + 590 + 225 clocks beside the MMAs, over two buffers, which fill
-// TMEM).  One CTA takes 820 for 128 weight rows, which its MMA thread is
-// never kept waiting for: 128 KB through shared memory.
+// 8192 x 4096 x 7168: 203-217 us (clocks between 1.6 and 1.9 GHz), 2.2-2.4
+// PFLOP/s; 380,000 clocks, about 820 per stage of two scale blocks inside a
+// tile, of which the MMAs need 512 at the full rate, and 3000 more per tile
+// for its output.  The issuing thread finds every stage and buffer ready, and
+// a second one made it 414,000, 16 epilogue warps instead of 8 nothing: what is
+// left is the 128 KB a stage moves through shared memory, copies in and
+// operands out (about 160 bytes a clock).  CTA pairs (256 rows x 128 weight
+// rows, cta_group::2) move 96 KB, but took 372,000 to 437,000 clocks: a buffer
+// comes back 1060 clocks after its last MMA there, and two buffers fill TMEM.
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
 // up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
@@ -65,10 +62,7 @@
 namespace moe {
 namespace {
 
-enum Mode { kSingle = 0, kSplit = 1, kPair = 2 };  // Fp8bForm::mode
-
-// Row blocks a pair launch can list (see list_pairs).
-constexpr int kMaxPairs = 4096;
+enum Mode { kSingle = 0, kSplit = 1 };  // Fp8bForm::mode
 
 template <int BN_, int MODE>
 struct Cfg {
@@ -76,42 +70,35 @@ struct Cfg {
   static constexpr int kBK = 128;  // one scale block
   static constexpr int kSub = 2;   // scale blocks of a stage (two units of work)
   static constexpr int kUmmaK = 32;
-  static constexpr int kBRows = MODE == kPair ? BN_ / 2 : BN_;  // weight rows per CTA
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kAShortRows = 32;
   static constexpr int kAShortBytes = kAShortRows * kBK;
-  static constexpr int kBBytes = kBRows * kBK;
+  static constexpr int kBBytes = BN_ * kBK;
   static constexpr int kStageBytes = kSub * (kABytes + kBBytes);
   static constexpr int kStages = 192 * 1024 / kStageBytes;
   // buffers of kSub scale blocks: stage j waits for the epilogue of j - kBufs
   static constexpr int kBufs = 2;
   static constexpr int kBufCols = kSub * BN_;
   static constexpr int kTmemCols = kBufs * kBufCols;
-  // Scale slots.  Stage j takes the slot of stage j - kSlots, free once the MMAs
-  // of stage i = j - kSlots + kBufs are done, and waits for those on the
-  // barrier of i's stage, which must not be a round ahead by then: the MMAs
-  // have come to stage j - 1 (they wait for the scales of j), or in a pair,
-  // where only the epilogue waits for them, to j + 1.  (With kStages slots
-  // everywhere, one CTA of 128 weight rows could write the scales of a stage
-  // only after the MMAs of the stage before it: 249 us instead of 217 for 8192
-  // x 4096 x 7168.)
-  static constexpr int kSlots = MODE == kPair ? kStages : kStages + kBufs;
-  static_assert(kStages > kBufs && kSlots <= kStages + kBufs, "see above");
+  // Scale slots.  Stage j takes the slot of stage j - kSlots, which has been
+  // read once the MMAs of stage j - kSlots + kBufs = j - kStages are done (they
+  // wait for the buffer of j - kSlots).  With kStages slots, the scales of a
+  // stage could be written only after the MMAs of the stage before it: 249 us
+  // instead of 217 for 8192 x 4096 x 7168.
+  static constexpr int kSlots = kStages + kBufs;
   static constexpr int kMmaWarp = 1;
   static constexpr int kScaleWarp = 2;
   static constexpr int kFirstEpi = 3;
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
   static constexpr int kCols = BN_ / 2;  // columns of an epilogue thread
-  static constexpr int kListBytes = MODE == kPair ? kMaxPairs * 2 : 0;
   static constexpr int kOutBytes = kEpiWarps * 2048;  // see store_rows
-  static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + kListBytes + 1024;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
 };
 
-// A CTA's part of a tile: expert, first row, valid rows (0: none), and the
-// valid rows of the pair's other CTA.
+// A tile's rows: expert, first row, valid rows (0: none).
 struct RowBlock {
-  int e, r0, valid, other;
+  int e, r0, valid;
 };
 
 // Valid rows of part `sub` (128 rows each) of align block `bi`.
@@ -124,7 +111,6 @@ __device__ __forceinline__ int part_valid(const Fp8bArgs& a, const int4& bi, int
 // block (blocks of 256 rows have two parts).
 __device__ __forceinline__ RowBlock row_block(const Fp8bArgs& a, int mb) {
   RowBlock r;
-  r.other = 0;
   if (a.block_info == nullptr) {
     r.e = 0;
     r.r0 = mb * 128;
@@ -139,78 +125,45 @@ __device__ __forceinline__ RowBlock row_block(const Fp8bArgs& a, int mb) {
   return r;
 }
 
-// Row blocks of pair `p`, for the CTA of rank `rank`: 256 rows of a plain
-// product, the two parts of a 256-row align block, or a listed block and the
-// next one of its expert.
-__device__ __forceinline__ RowBlock pair_block(const Fp8bArgs& a, int p, int rank,
-                                               const uint16_t* list) {
-  RowBlock r;
-  if (a.block_info == nullptr) {
-    r.e = 0;
-    r.r0 = p * 256 + 128 * rank;
-    r.valid = max(0, min(128, a.M - r.r0));
-    r.other = max(0, min(128, a.M - p * 256 - 128 * (rank ^ 1)));
-    return r;
+// Division by a divisor known once per launch, for tile indexes below 2^31.
+// umulhi(x, floor((2^32 - 1) / d)) falls short of x / d by less than 2.
+struct FastDiv {
+  unsigned d, m;
+  __device__ explicit FastDiv(unsigned d_) : d(d_), m(0xffffffffu / d_) {}
+  __device__ __forceinline__ unsigned operator()(unsigned x) const {
+    unsigned q = __umulhi(x, m);
+    unsigned r = x - q * d;
+    if (r >= d) ++q, r -= d;
+    if (r >= d) ++q;
+    return q;
   }
-  const int4* info = reinterpret_cast<const int4*>(a.block_info);
-  if (a.subs == 2) {
-    const int4 bi = info[p];
-    r.e = bi.x;
-    r.r0 = bi.z + 128 * rank;
-    r.valid = part_valid(a, bi, rank);
-    r.other = part_valid(a, bi, rank ^ 1);
-    return r;
-  }
-  const int b = list[p] >> 1;
-  const bool two = list[p] & 1;
-  const int4 b0 = info[b];
-  const int v0 = part_valid(a, b0, 0);
-  int4 b1 = b0;
-  int v1 = 0;
-  if (two) {
-    b1 = info[b + 1];
-    v1 = part_valid(a, b1, 0);
-  }
-  r.e = b0.x;
-  r.r0 = rank == 0 ? b0.z : b1.z;
-  r.valid = rank == 0 ? v0 : v1;
-  r.other = rank == 0 ? v1 : v0;
-  return r;
-}
+};
 
-// The pairs of a list of `nb` align blocks of at most 128 rows: every block of
-// even index within its expert, with the next one where the expert has it.
-// Entry = 2 * block + (has a second one); at most kMaxPairs blocks.  All threads of the CTA; returns
-// the number of pairs.
-__device__ __forceinline__ int list_pairs(const Fp8bArgs& a, int nb, uint16_t* list,
-                                          int* s_warp_sum) {
-  const int4* info = reinterpret_cast<const int4*>(a.block_info);
-  const int per = (nb + blockDim.x - 1) / blockDim.x;
-  const int lo = min(nb, static_cast<int>(threadIdx.x) * per), hi = min(nb, lo + per);
-  int cnt = 0;
-  for (int b = lo; b < hi; ++b) cnt += (info[b].y & 1) == 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = cnt;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
+// decode_tile's order (sched.cuh; no K splits) without its divisions, which
+// took the one thread that issues the MMAs about 1000 clocks a tile.
+struct TileOrder {
+  int num_blocks, n_tiles, band, full_bands;
+  FastDiv by_band_tiles, by_band, by_tail;
+  __device__ TileOrder(int blocks, const Fp8bArgs& a)
+      : num_blocks(blocks),
+        n_tiles(a.n_tiles),
+        band(a.band),
+        full_bands(a.n_tiles / a.band),
+        by_band_tiles(static_cast<unsigned>(max(1, blocks * a.band))),
+        by_band(static_cast<unsigned>(a.band)),
+        by_tail(static_cast<unsigned>(max(1, a.n_tiles % a.band))) {}
+  __device__ __forceinline__ Tile operator()(int tile) const {
+    Tile t;
+    t.split = 0;
+    const int b = static_cast<int>(by_band_tiles(static_cast<unsigned>(tile)));
+    const bool full = b < full_bands;
+    const int nt0 = (full ? b : full_bands) * band;
+    const unsigned w = static_cast<unsigned>(tile - nt0 * num_blocks);
+    t.mb = static_cast<int>(full ? by_band(w) : by_tail(w));
+    t.nt = nt0 + static_cast<int>(w) - t.mb * (full ? band : n_tiles - full_bands * band);
+    return t;
   }
-  if (lane == 31) s_warp_sum[warp] = incl;
-  __syncthreads();
-  int at = incl - cnt, total = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    if (w < warp) at += s_warp_sum[w];
-    total += s_warp_sum[w];
-  }
-  for (int b = lo; b < hi; ++b) {
-    const int m = info[b].y;
-    if (m & 1) continue;
-    const bool two = b + 1 < nb && info[b + 1].y == m + 1;
-    list[at++] = static_cast<uint16_t>(2 * b + (two ? 1 : 0));
-  }
-  return total;
-}
+};
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   uint64_t v;
@@ -229,6 +182,33 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+// Rows of any alignment: the sums of a warp's rows through `stage` (2 KB), 16
+// columns at a time, so that lanes store consecutive elements of a row.  Out
+// of line, as its registers would cost the main loop 5 to 15 % of its speed.
+template <int COLS>
+__device__ __noinline__ void store_rows_any(void* out, int N, int out_bf16, long long row0,
+                                            int rows, int col, const float* acc, float* stage,
+                                            int lane) {
+  const int c = lane & 15;
+  for (int c0 = 0; c0 < COLS && col + c0 < N; c0 += 16) {
+    __syncwarp();
+    // column-major pieces of 32 rows: neither side meets a bank twice
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stage[i * 32 + ((lane + i) & 31)] = acc[c0 + i];
+    __syncwarp();
+    if (col + c0 + c < N) {
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const float v = stage[c * 32 + ((r + c) & 31)];
+        const long long o = (row0 + r) * N + col + c0 + c;
+        if (out_bf16)
+          static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(v);
+        else
+          static_cast<float*>(out)[o] = v;
+      }
+    }
+  }
+}
+
 // The COLS sums of each of a warp's 32 rows (a lane per row) to columns
 // [col, col + COLS) of out, those below N, for the first `rows` rows.  16-byte
 // stores go through `stage`, 2 KB of shared memory of the warp: 64 bytes of
@@ -244,22 +224,11 @@ __device__ __forceinline__ void store_rows(const Fp8bArgs& a, long long row0, in
   const int n = min(COLS, a.N - col);
   const int es = a.out_bf16 ? 2 : 4;
   if (!a.wide_out) {
-    if (lane >= rows) return;
-    const long long o = (row0 + lane) * a.N + col;
+    float v[COLS];
 #pragma unroll
-    for (int i = 0; i < COLS / 2; ++i) {
-      float v[2];
-      unpack2(acc[i], v[0], v[1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (2 * i + j < n) {
-          if (a.out_bf16)
-            static_cast<__nv_bfloat16*>(a.out)[o + 2 * i + j] = __float2bfloat16_rn(v[j]);
-          else
-            static_cast<float*>(a.out)[o + 2 * i + j] = v[j];
-        }
-      }
-    }
+    for (int i = 0; i < COLS / 2; ++i) unpack2(acc[i], v[2 * i], v[2 * i + 1]);
+    store_rows_any<COLS>(a.out, a.N, a.out_bf16, row0, rows, col, v,
+                         reinterpret_cast<float*>(stage), lane);
     return;
   }
   char* base = static_cast<char*>(a.out) + (row0 * a.N + col) * es;
@@ -317,31 +286,25 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tmAShort,
                      const __grid_constant__ CUtensorMap tmB) {
   using C = Cfg<BN, MODE>;
-  constexpr bool PAIR = MODE == kPair;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::kStages];
   __shared__ __align__(8) uint64_t empty_bar[C::kStages];
   __shared__ __align__(8) uint64_t acce_bar[C::kBufs];
-  __shared__ __align__(8) uint64_t scale_bar[C::kStages];
   // sa * sb of the tile's rows for the scale blocks of a stage
   __shared__ float s_scale[C::kSlots][C::kSub][128];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_skip;
-  __shared__ int s_warp_sum[C::kThreads / 32];
   __shared__ volatile int s_abort;
 
   // through a shuffle, so that the compiler knows it to be the same for a warp
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = MODE == kSingle ? 0u : cluster_ctarank();
-  const bool leader = !PAIR || rank == 0;
   const uint32_t smemA = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t smemB = smemA + C::kStages * C::kSub * C::kABytes;
   uint8_t* smem_gen = smem_raw + (smemA - smem_u32(smem_raw));
   uint4* out_stage = reinterpret_cast<uint4*>(smem_gen + C::kStages * C::kStageBytes);
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem_gen + C::kStages * C::kStageBytes +
-                                               C::kOutBytes);
 
   pdl_wait();
   pdl_launch_dependents();
@@ -349,13 +312,11 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
     s_skip = (a.status != nullptr && *reinterpret_cast<volatile int32_t*>(a.status) != 0);
     s_abort = 0;
     for (int i = 0; i < C::kStages; ++i) {
-      // the expected bytes and (one CTA: see the scale warp) the scales
-      mbar_init(smem_u32(&full_bar[i]), PAIR ? 1 : 2);
-      mbar_init(smem_u32(&scale_bar[i]), 1);
+      mbar_init(smem_u32(&full_bar[i]), 2);  // the expected bytes and the scales
       mbar_init(smem_u32(&empty_bar[i]), 1);
     }
     for (int i = 0; i < C::kBufs; ++i)
-      mbar_init(smem_u32(&acce_bar[i]), (PAIR ? 2 : 1) * C::kEpiWarps);
+      mbar_init(smem_u32(&acce_bar[i]), C::kEpiWarps);
     mbar_init(smem_u32(&drain_bar), 1);
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -370,37 +331,25 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       (MODE == kSingle ? s_skip
                        : static_cast<int>(ld_shared_cluster_u32(
                              mapa_shared(smem_u32(&s_skip), 0)))) != 0;
-  if (!skip && warp == C::kMmaWarp) {
-    if constexpr (PAIR)
-      tmem_alloc_pair(smem_u32(&s_tmem_base), C::kTmemCols);
-    else
-      tmem_alloc(smem_u32(&s_tmem_base), C::kTmemCols);
-  }
+  if (!skip && warp == C::kMmaWarp) tmem_alloc(smem_u32(&s_tmem_base), C::kTmemCols);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmAShort);
     tma_prefetch_desc(&tmB);
   }
-  int num_blocks = 0;  // row blocks, or pairs of them
-  if (!skip) {
-    if (a.block_info == nullptr) {
-      num_blocks = PAIR ? (a.max_blocks + 1) / 2 : a.max_blocks;
-    } else {
-      num_blocks = checked_num_blocks(*a.num_blocks, a.max_blocks, a.status);
-      if constexpr (PAIR) {
-        if (a.subs == 1) num_blocks = list_pairs(a, num_blocks, list, s_warp_sum);
-      } else {
-        num_blocks *= a.subs;
-      }
-    }
-  }
+  int num_blocks = 0;
+  if (!skip)
+    num_blocks = a.block_info == nullptr
+                     ? a.max_blocks
+                     : checked_num_blocks(*a.num_blocks, a.max_blocks, a.status) * a.subs;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = s_tmem_base;
 
+  const TileOrder order(num_blocks, a);
   const int total = num_blocks * a.n_tiles;
-  const int csize = MODE == kSingle ? 1 : (PAIR ? 2 : a.splits);
+  const int csize = MODE == kSingle ? 1 : a.splits;
   const int first = blockIdx.x / csize;
   const int step = gridDim.x / csize;
   // this CTA's scale blocks
@@ -408,15 +357,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   const int ke = MODE == kSplit ? a.k_tiles * (static_cast<int>(rank) + 1) / a.splits : a.k_tiles;
   const uint64_t to = a.timeout_ns;
 
-  auto block_of = [&](int mb) {
-    if constexpr (PAIR)
-      return pair_block(a, mb, static_cast<int>(rank), list);
-    else
-      return row_block(a, mb);
-  };
   // MMA columns of weight tile nt: a multiple of 16
   auto tile_cols = [&](int nt) { return min(BN, (a.N - nt * BN + 15) & ~15); };
-  auto live_tile = [&](const RowBlock& r) { return r.valid > 0 || r.other > 0; };
 
   if (warp < C::kFirstEpi) {
     if (warp == 0) {
@@ -426,39 +368,27 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         uint32_t stage = 0, phase = 0;
         unsigned issued = 0;
         bool ok = true;
-        const uint32_t full0 =
-            PAIR ? mapa_shared(smem_u32(&full_bar[0]), 0) : smem_u32(&full_bar[0]);
         for (int tile = first; tile < total && ok; tile += step) {
-          const Tile t = decode_tile(tile, num_blocks, a);
-          const RowBlock r = block_of(t.mb);
-          if (!live_tile(r)) continue;
-          auto a_bytes = [&](int valid) {
-            return valid <= C::kAShortRows ? C::kAShortBytes : C::kABytes;
-          };
-          const CUtensorMap* map_a = r.valid <= C::kAShortRows ? &tmAShort : &tmA;
-          const uint32_t tx = PAIR ? 2 * C::kBBytes + a_bytes(r.valid) + a_bytes(r.other)
-                                   : C::kBBytes + a_bytes(r.valid);
-          // (kPair: this CTA's half of the tile's weight rows)
-          const int w_row = r.e * a.N + t.nt * BN +
-                            (PAIR ? static_cast<int>(rank) * (tile_cols(t.nt) >> 1) : 0);
+          const Tile t = order(tile);
+          const RowBlock r = row_block(a, t.mb);
+          if (r.valid <= 0) continue;
+          const bool short_a = r.valid <= C::kAShortRows;
+          const CUtensorMap* map_a = short_a ? &tmAShort : &tmA;
+          const uint32_t tx = C::kBBytes + (short_a ? C::kAShortBytes : C::kABytes);
+          const int w_row = r.e * a.N + t.nt * BN;
           for (int kt = kb; kt < ke; kt += C::kSub) {
             if (!mbar_wait_suspend(smem_u32(&empty_bar[stage]), phase ^ 1, &s_abort, to)) {
               ok = false;
               break;
             }
-            const uint32_t fb = full0 + stage * 8u;
+            const uint32_t fb = smem_u32(&full_bar[stage]);
             const int nk = min(C::kSub, ke - kt);
-            if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), tx * nk);
+            mbar_arrive_expect_tx(fb, tx * nk);
             for (int u = 0; u < nk; ++u) {
               const uint32_t da = smemA + (stage * C::kSub + u) * C::kABytes;
               const uint32_t db = smemB + (stage * C::kSub + u) * C::kBBytes;
-              if constexpr (PAIR) {
-                tma_load_2d_pair(da, map_a, fb, (kt + u) * C::kBK, r.r0);
-                tma_load_2d_pair(db, &tmB, fb, (kt + u) * C::kBK, w_row);
-              } else {
-                tma_load_2d(da, map_a, fb, (kt + u) * C::kBK, r.r0);
-                tma_load_2d(db, &tmB, fb, (kt + u) * C::kBK, w_row);
-              }
+              tma_load_2d(da, map_a, fb, (kt + u) * C::kBK, r.r0);
+              tma_load_2d(db, &tmB, fb, (kt + u) * C::kBK, w_row);
             }
             ++issued;
             if (++stage == C::kStages) {
@@ -468,31 +398,27 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           }
         }
         if (!ok) {
-          if constexpr (PAIR) {
-            settle(to / 8);
-          } else {
-            const unsigned n0 = issued > C::kStages ? issued - C::kStages : 0;
-            for (unsigned n = n0; n < issued; ++n)
-              drain_wait(smem_u32(&full_bar[n % C::kStages]), (n / C::kStages) & 1, to / 4);
-          }
+          const unsigned n0 = issued > C::kStages ? issued - C::kStages : 0;
+          for (unsigned n = n0; n < issued; ++n)
+            drain_wait(smem_u32(&full_bar[n % C::kStages]), (n / C::kStages) & 1, to / 4);
         }
       }
-    } else if (warp == C::kMmaWarp && leader && elect_one()) {
+    } else if (warp == C::kMmaWarp && elect_one()) {
       // ----------------------------------------------------- MMA issuer
       // stage 0's descriptors; their address field counts 16 bytes
       const uint64_t a_desc0 = sw128_kmajor_desc(smemA), b_desc0 = sw128_kmajor_desc(smemB);
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
       bool ok = true;
       for (int tile = first; tile < total && ok; tile += step) {
-        const Tile t = decode_tile(tile, num_blocks, a);
-        if (!live_tile(block_of(t.mb))) continue;
-        const uint32_t idesc = make_idesc(0, PAIR ? 256 : 128, tile_cols(t.nt));  // e4m3 x e4m3
+        const Tile t = order(tile);
+        if (row_block(a, t.mb).valid <= 0) continue;
+        const uint32_t idesc = make_idesc(0, 128, tile_cols(t.nt));  // e4m3 x e4m3
         for (int kt = kb; kt < ke; kt += C::kSub) {
           // both looks in flight at once
           const uint32_t bf = smem_u32(&full_bar[stage]);
           const uint32_t be = smem_u32(&acce_bar[buf]);
-          const bool rf = mbar_look<PAIR>(bf, phase);
-          const bool re = mbar_look<PAIR>(be, buf_phase ^ 1);
+          const bool rf = mbar_try_wait(bf, phase);
+          const bool re = mbar_try_wait(be, buf_phase ^ 1);
           const uint32_t d_tmem = tmem_base + buf * C::kBufCols;
           const uint64_t ad = a_desc0 + stage * (C::kSub * C::kABytes >> 4);
           const uint64_t bd = b_desc0 + stage * (C::kSub * C::kBBytes >> 4);
@@ -501,20 +427,11 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
             for (int k = 0; k < C::kBK / C::kUmmaK; ++k) {
               const uint64_t da = ad + u * (C::kABytes >> 4) + k * (C::kUmmaK >> 4);
               const uint64_t db = bd + u * (C::kBBytes >> 4) + k * (C::kUmmaK >> 4);
-              if constexpr (PAIR)
-                umma_f8_pair(d_tmem + u * BN, da, db, idesc, k > 0 ? 1u : 0u);
-              else
-                umma_f8(d_tmem + u * BN, da, db, idesc, k > 0 ? 1u : 0u);
+              umma_f8(d_tmem + u * BN, da, db, idesc, k > 0 ? 1u : 0u);
             }
           };
-          auto commit = [&](uint32_t bar) {
-            if constexpr (PAIR)
-              umma_commit_pair(bar, 0x3);
-            else
-              umma_commit(bar);
-          };
-          if (!(rf || mbar_wait_suspended<PAIR>(bf, phase, &s_abort, to)) ||
-              !(re || mbar_wait_suspended<PAIR>(be, buf_phase ^ 1, &s_abort, to))) {
+          if (!(rf || mbar_wait_suspended(bf, phase, &s_abort, to)) ||
+              !(re || mbar_wait_suspended(be, buf_phase ^ 1, &s_abort, to))) {
             ok = false;
             break;
           }
@@ -522,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           mma(0);
           if (kt + 1 < ke) mma(1);
           // frees the stage and hands the buffer to the epilogue
-          commit(smem_u32(&empty_bar[stage]));
+          umma_commit(smem_u32(&empty_bar[stage]));
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1;
@@ -534,33 +451,27 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         }
       }
       if (!ok) {
-        if constexpr (PAIR)
-          umma_commit_pair(smem_u32(&drain_bar), 0x1);
-        else
-          umma_commit(smem_u32(&drain_bar));
+        umma_commit(smem_u32(&drain_bar));
         drain_wait(smem_u32(&drain_bar), 0, to / 4);
       }
     } else if (warp == C::kScaleWarp && !a.starve) {
       // ----------------------------------------------------- scales
       // A lane has four rows; the scale blocks of kGroup stages are loaded
       // together (a 32-byte sector of each row), while those of the kGroup
-      // stages before them are written.  The epilogue has read the slot of
-      // stage j - kSlots once the MMAs of stage j - kSlots + kBufs are done,
-      // as they wait for its buffer.
+      // stages before them are written.
       constexpr int kGroup = 4, kBlocks = kGroup * C::kSub;
       uint32_t stage = 0, slot = 0;
-      // The first kStages stages wait for nothing.  From then on stage j
-      // waits for the MMAs of j - kSlots + kBufs, in one CTA those of
-      // j - kStages: its arrival below must not come before the phase of the
-      // full barrier it counts in.
-      int w_stage = C::kStages - C::kSlots + C::kBufs;
+      // The first kStages stages wait for nothing, the others for the MMAs of
+      // stage j - kStages: for their slot, and so that the arrival below does
+      // not come before the phase of the full barrier it counts in.
+      int w_stage = 0;
       uint32_t w_phase = 0;
       int fresh = C::kStages;
       bool ok = true;
       for (int tile = first; tile < total && ok; tile += step) {
-        const Tile t = decode_tile(tile, num_blocks, a);
-        const RowBlock r = block_of(t.mb);
-        if (!live_tile(r)) continue;
+        const Tile t = order(tile);
+        const RowBlock r = row_block(a, t.mb);
+        if (r.valid <= 0) continue;
         const float* sb = a.w_scale + (static_cast<long long>(r.e) * a.n_scales +
                                        t.nt * BN / 128) * a.k_tiles;
         const float* sa = a.a_scale + (static_cast<long long>(r.r0) + lane) * a.k_tiles;
@@ -606,11 +517,10 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 s_scale[slot][u][32 * i + lane] = s[g * C::kSub + u][i];
-            // One CTA: the slot joins its stage's full barrier, and whoever
-            // sees that stage's MMAs done sees it too.  A pair's full barrier
-            // is the leader's alone: a barrier of its own.
+            // the slot joins its stage's full barrier: whoever sees that
+            // stage's MMAs done sees it too
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(PAIR ? &scale_bar[stage] : &full_bar[stage]));
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar[stage]));
             if (++stage == C::kStages) stage = 0;
             if (++slot == C::kSlots) slot = 0;
           }
@@ -622,13 +532,11 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int col_in_tile = ((warp - C::kFirstEpi) >> 2) * C::kCols;
-    const uint32_t acce0 =
-        PAIR ? mapa_shared(smem_u32(&acce_bar[0]), 0) : smem_u32(&acce_bar[0]);
     uint32_t buf = 0, stage = 0, phase = 0, slot = 0;
     for (int tile = first; tile < total; tile += step) {
-      const Tile t = decode_tile(tile, num_blocks, a);
-      const RowBlock r = block_of(t.mb);
-      if (!live_tile(r)) continue;
+      const Tile t = order(tile);
+      const RowBlock r = row_block(a, t.mb);
+      if (r.valid <= 0) continue;
       const int local = q * 32 + lane;
       const int col = t.nt * BN + col_in_tile;
       // warps without a row or a column of the output only keep the barriers
@@ -640,22 +548,13 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       // ran out the loop goes on to its end without waiting, so that the warp
       // stays converged; nothing is stored then.
       auto wait = [&] {
-        const uint32_t bd = smem_u32(&empty_bar[stage]), bs = smem_u32(&scale_bar[stage]);
-        const bool r0 = mbar_look<false>(bd, phase);
-        const bool r1 = !PAIR || mbar_look<false>(bs, phase);
-        if (!r0) mbar_wait_suspended<false>(bd, phase, &s_abort, to);
-        if (!r1) mbar_wait_suspended<false>(bs, phase, &s_abort, to);
+        mbar_wait_suspend(smem_u32(&empty_bar[stage]), phase, &s_abort, to);
         __syncwarp();
         tc_fence_after_sync();
       };
       auto release = [&] {
         tc_fence_before_sync();
-        if (lane == 0) {
-          if constexpr (PAIR)
-            mbar_arrive_cluster_relaxed(acce0 + buf * 8u);
-          else
-            mbar_arrive_relaxed(acce0 + buf * 8u);
-        }
+        if (lane == 0) mbar_arrive_relaxed(smem_u32(&acce_bar[buf]));
       };
       auto next_stage = [&] {
         buf ^= 1;
@@ -761,8 +660,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
     // the cluster's tile: each CTA adds up and stores 64 / splits of its
     // columns, the partial sums in rank order
     if (first < total && !s_abort) {
-      const Tile t = decode_tile(first, num_blocks, a);
-      const RowBlock r = block_of(t.mb);
+      const Tile t = order(first);
+      const RowBlock r = row_block(a, t.mb);
       const int span = BN / a.splits;
       const int c0 = static_cast<int>(rank) * span;
       for (int i = threadIdx.x; i < span * r.valid; i += blockDim.x) {
@@ -785,10 +684,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   if (threadIdx.x == 0 && s_abort) report_error(a.status, MOE_ERR_TIMEOUT);
   if (!skip && warp == C::kMmaWarp) {
     tc_fence_after_sync();
-    if constexpr (PAIR)
-      tmem_dealloc_pair(tmem_base, C::kTmemCols);
-    else
-      tmem_dealloc(tmem_base, C::kTmemCols);
+    tmem_dealloc(tmem_base, C::kTmemCols);
   }
 }
 
@@ -817,7 +713,7 @@ cudaError_t launch(Fp8bArgs a, const Fp8bForm& f, const Fp8bMaps& maps, cudaStre
   a.band = std::min(a.n_tiles, 8);
   a.splits = f.splits;
   cudaLaunchAttribute attr[2];
-  const unsigned cluster = MODE == kPair ? 2 : MODE == kSplit ? f.splits : 1;
+  const unsigned cluster = MODE == kSplit ? f.splits : 1;
   const cudaLaunchConfig_t cfg =
       pdl_config(dim3(f.grid), dim3(C::kThreads), C::kSmemBytes, s, attr, cluster);
   return cudaLaunchKernelEx(&cfg, fp8b_gemm_kernel<BN, MODE>, a, maps.a, maps.a_short, maps.b);
@@ -825,76 +721,58 @@ cudaError_t launch(Fp8bArgs a, const Fp8bForm& f, const Fp8bMaps& maps, cudaStre
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }
 
-// Clusters of `ctas` CTAs of the split form (4 and 8) or CTA pairs of the pair
-// form (2) the current device holds at once, 0 if unknown.
-template <int BN, int MODE>
-int max_clusters(int ctas) {
-  using C = Cfg<BN, MODE>;
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(ctas), dim3(C::kThreads), C::kSmemBytes, nullptr, attr, ctas);
-  int n = 0;
-  if (prepare_kernel<BN, MODE>() != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, fp8b_gemm_kernel<BN, MODE>, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  return n;
-}
 }  // namespace
 
+// Clusters of 2, 4 and 8 CTAs of the split form the current device holds at
+// once, 0 where unknown.
 Fp8bHeld fp8b_held() {
-  Fp8bHeld h;
-  h.pairs = max_clusters<128, kPair>(2);
-  h.split[0] = max_clusters<64, kSplit>(2);
-  h.split[1] = max_clusters<64, kSplit>(4);
-  h.split[2] = max_clusters<64, kSplit>(8);
+  using C = Cfg<64, kSplit>;
+  Fp8bHeld h = {};
+  if (prepare_kernel<64, kSplit>() != cudaSuccess) {
+    cudaGetLastError();
+    return h;
+  }
+  for (int i = 0; i < 3; ++i) {
+    const int ctas = 2 << i;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        pdl_config(dim3(ctas), dim3(C::kThreads), C::kSmemBytes, nullptr, attr, ctas);
+    if (cudaOccupancyMaxActiveClusters(&h.split[i], fp8b_gemm_kernel<64, kSplit>, &cfg) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      h.split[i] = 0;
+    }
+  }
   return h;
 }
 
 // The form with the least estimated time: rounds of tiles times what a stage
-// takes (GB300, us: 0.36 with 64 weight rows, 0.55 with 128, 0.53 for a pair;
-// 8192 x 4096 x 7168 took 272, 217 and 208).  Measured around the choice:
-// 333 x 2880 x 2880 in 8.2 us with 64 rows, 9.8 with 128 and 11.6 as pairs;
-// 1024 x 4096 x 7168 in 43, 33.4 and 33.8; 8192 rows of 32 experts against 4096
-// x 7168 in 407, 296 and 344 (a pair's second half is often padding there).  A
-// sorted list's row blocks are estimated from its capacity: at least one row
-// per align block and all but the padding of E blocks; half a block of padding
-// per expert that has rows.
+// takes (GB300, us: 0.36 with 64 weight rows, 0.55 with 128; 8192 x 4096 x 7168
+// took 268 and 204).  Measured around the choice: 333 x 2880 x 2880 in 8.1 us
+// with 64 rows and 9.8 with 128; 1024 x 4096 x 7168 in 43 and 33; 8192 rows of 32
+// experts against 4096 x 7168 in 407 and 296.  A sorted list's row blocks are
+// estimated from its capacity: at least one row per align block and all but
+// the padding of E blocks; half a block of padding per expert that has rows.
 Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
   Fp8bForm f;
-  const int pairs = held.pairs;
   f.splits = 1;
+  f.mode = kSingle;
   const long long n64 = div_up(a.N, 64), n128 = div_up(a.N, 128);
   const long long max_blocks = static_cast<long long>(a.max_blocks) * a.subs;
-  double blocks = static_cast<double>(max_blocks), two = static_cast<double>(div_up(max_blocks, 2));
-  const bool can_pair = pairs > 0 && (a.block_info == nullptr || a.subs == 2 ||
-                                      a.max_blocks <= kMaxPairs);
+  double blocks = static_cast<double>(max_blocks);
   if (a.block_info != nullptr) {
     const long long rows =
         std::max<long long>(a.max_blocks, a.cap - static_cast<long long>(a.E) * (a.block_m - 1));
     const double experts = static_cast<double>(std::min<long long>(a.E, rows));
-    const double part = std::min(128, a.block_m);
-    blocks = std::min(blocks, rows / part + experts / 2);
-    two = a.block_m < 128 ? blocks : std::min(blocks, rows / 256.0 + experts / 2);
+    blocks = std::min(blocks, static_cast<double>(rows) / std::min(128, a.block_m) + experts / 2);
   }
-  auto rounds = [](double tiles, int at_once) { return std::ceil(tiles / at_once); };
-  const double us64 = 0.36 * rounds(blocks * n64, sms);
-  const double us128 = 0.55 * rounds(blocks * n128, sms);
-  const double us_pair = can_pair ? 0.53 * rounds(two * n128, pairs) : 1e30;
-  const long long pair_tiles =
-      (a.block_info != nullptr && a.subs == 1 ? max_blocks : div_up(max_blocks, 2)) * n128;
-  if (us_pair <= us64 && us_pair <= us128) {
+  const double us64 = 0.36 * std::ceil(blocks * n64 / sms);
+  const double us128 = 0.55 * std::ceil(blocks * n128 / sms);
+  if (us128 <= us64) {
     f.bn = 128;
-    f.mode = kPair;
-    f.grid = static_cast<int>(2 * std::min<long long>(pairs, pair_tiles));
-  } else if (us128 <= us64) {
-    f.bn = 128;
-    f.mode = kSingle;
     f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n128));
   } else {
     f.bn = 64;
-    f.mode = kSingle;
     f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n64));
     // Splitting K by s, where all the clusters are resident at once: 0.29 us
     // for every stage a CTA has less, against 2.5 us of cluster launch,
@@ -914,13 +792,11 @@ Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
       }
     }
   }
-  f.b_rows = f.mode == kPair ? f.bn / 2 : f.bn;
   return f;
 }
 
 cudaError_t launch_fp8b_gemm(const Fp8bArgs& a, const Fp8bForm& f, const Fp8bMaps& maps,
                              cudaStream_t s) {
-  if (f.mode == kPair) return launch<128, kPair>(a, f, maps, s);
   if (f.mode == kSplit) return launch<64, kSplit>(a, f, maps, s);
   return f.bn == 128 ? launch<128, kSingle>(a, f, maps, s) : launch<64, kSingle>(a, f, maps, s);
 }

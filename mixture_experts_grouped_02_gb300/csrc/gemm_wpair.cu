@@ -128,6 +128,12 @@ __device__ __forceinline__ float activate(const Epilogue& ep, float g, float u) 
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
+__device__ __forceinline__ void settle(uint64_t ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < ns) {
+  }
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }

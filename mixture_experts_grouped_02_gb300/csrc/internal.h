@@ -250,19 +250,19 @@ struct Fp8bArgs {
   int starve;                  // failure-path test: the producer issues no copies
 };
 // How a product is cut: weight rows of a tile, mode (gemm_fp8b.cu), CTAs that
-// share a tile's K range, CTAs in all, weight rows of a tensor-map box.
+// share a tile's K range, CTAs in all.
 struct Fp8bForm {
-  int bn, mode, splits, grid, b_rows;
+  int bn, mode, splits, grid;
 };
-// CTA pairs, and clusters of 2, 4 and 8 CTAs of the split form, the current
-// device holds at once (0: unknown).
+// Clusters of 2, 4 and 8 CTAs of the split form the current device holds at
+// once (0: unknown).
 struct Fp8bHeld {
-  int pairs, split[3];
+  int split[3];
 };
 Fp8bHeld fp8b_held();
 Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held);
 // Tensor maps: a in boxes of 128 and 32 rows of 128 bytes; the E * N weight
-// rows in boxes of b_rows.
+// rows in boxes of the form's bn.
 struct Fp8bMaps {
   CUtensorMap a, a_short, b;
 };

@@ -83,7 +83,7 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
   int rc = make_byte_map(&maps.a, x, a.K, rows, 128, 128);
   if (rc == MOE_OK) rc = make_byte_map(&maps.a_short, x, a.K, rows, 128, 32);
   if (rc == MOE_OK)
-    rc = make_byte_map(&maps.b, w, a.K, static_cast<long long>(a.E) * a.N, 128, f.b_rows);
+    rc = make_byte_map(&maps.b, w, a.K, static_cast<long long>(a.E) * a.N, 128, f.bn);
   if (rc != MOE_OK) return rc;
   return cuda_status(launch_fp8b_gemm(a, f, maps, s));
 }
@@ -220,27 +220,22 @@ int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_
                             void* stream) {
   const int rc = check_gemm(1, N, K, out_dtype);
   if (rc != MOE_OK) return rc;
-  if (M <= 0 || form < 0 || form > 5) return MOE_ERR_INVALID_ARG;
+  if (M <= 0 || form < 0 || form > 4) return MOE_ERR_INVALID_ARG;
   if (wait_limit_ns != 0 && (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull))
     return MOE_ERR_INVALID_ARG;
   Fp8bArgs g = plain_args(a_scale, w_scale, M, N, K, out, dev_status);
   g.timeout_ns = wait_limit_ns;
   g.starve = wait_limit_ns != 0;
-  // {weight rows of a tile, mode, splits} of forms 0 to 5
-  static const int kForms[6][3] = {{64, 0, 1}, {128, 0, 1}, {128, 2, 1},
-                                   {64, 1, 2}, {64, 1, 4},  {64, 1, 8}};
+  // {weight rows of a tile, mode, splits} of forms 0 to 4
+  static const int kForms[5][3] = {{64, 0, 1}, {128, 0, 1}, {64, 1, 2}, {64, 1, 4}, {64, 1, 8}};
   Fp8bForm f;
   f.bn = kForms[form][0];
   f.mode = kForms[form][1];
   f.splits = kForms[form][2];
-  f.b_rows = form == 2 ? 64 : f.bn;
-  const long long tiles = static_cast<long long>(form == 2 ? (g.max_blocks + 1) / 2 : g.max_blocks) *
-                          ((N + f.bn - 1) / f.bn);
+  const long long tiles = static_cast<long long>(g.max_blocks) * ((N + f.bn - 1) / f.bn);
   if (tiles * f.splits > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
-  const int held = form == 2 ? held_clusters().pairs : device_sm_count();
-  if (held <= 0) return MOE_ERR_CUDA;
-  f.grid = static_cast<int>(form >= 3 ? tiles * f.splits
-                                      : (form == 2 ? 2 : 1) * (tiles < held ? tiles : held));
+  const int sms = device_sm_count();
+  f.grid = static_cast<int>(form >= 2 ? tiles * f.splits : tiles < sms ? tiles : sms);
   return run_gemm(g, a, M, w, out_dtype, as_stream(stream), &f);
 }
 

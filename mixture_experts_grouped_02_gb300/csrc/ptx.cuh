@@ -86,6 +86,36 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same wait in two steps for waits that mostly find the phase complete: a
+// first look (mbar_try_wait, 55 clocks measured; 87 with a suspend time), and
+// this loop, suspended in hardware between looks, when it was not.
+__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity,
+                                                    volatile int* abort_flag,
+                                                    uint64_t timeout_ns) {
+  constexpr uint32_t kSuspendNs = 100000;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > timeout_ns) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_suspend(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag, uint64_t timeout_ns) {
+  return mbar_try_wait(bar, parity) || mbar_wait_suspended(bar, parity, abort_flag, timeout_ns);
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -107,16 +137,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// Arrive without ordering this thread's memory operations, on a barrier of
-// this CTA or (cluster address) of any CTA of the cluster.
+// Arrive without ordering this thread's memory operations.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 // try_wait that acquires at cluster scope (for barriers other CTAs arrive on).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -145,56 +169,6 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t
       return false;
     }
   }
-}
-
-// The same wait in two steps for waits that mostly find the phase complete: a
-// first look by the caller (mbar_try_wait, 55 clocks measured; 87 with a
-// suspend time), and this loop, suspended in hardware between looks, when it
-// was not.
-constexpr uint32_t kSuspendNs = 100000;
-template <bool CLUSTER>
-__device__ __forceinline__ bool mbar_look(uint32_t bar, uint32_t parity) {
-  if constexpr (CLUSTER)
-    return mbar_try_wait_cluster(bar, parity);
-  else
-    return mbar_try_wait(bar, parity);
-}
-template <bool CLUSTER>
-__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity,
-                                                    volatile int* abort_flag,
-                                                    uint64_t timeout_ns) {
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    uint32_t ok;
-    if constexpr (CLUSTER)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity), "r"(kSuspendNs)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity), "r"(kSuspendNs)
-          : "memory");
-    if (ok) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > timeout_ns) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait_suspend(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort_flag, uint64_t timeout_ns) {
-  return mbar_look<CLUSTER>(bar, parity) ||
-         mbar_wait_suspended<CLUSTER>(bar, parity, abort_flag, timeout_ns);
 }
 
 // 32-bit load from a shared variable of another CTA of the cluster.
@@ -388,16 +362,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
-// The CTA-pair form (operands and result as umma_bf16_pair).
-__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Four consecutive 32-bit TMEM columns of the calling warp's 32 lanes.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t v0, uint32_t v1, uint32_t v2,
                                          uint32_t v3) {
@@ -480,26 +444,6 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                  "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
-// 16 columns, and the wait that the uses of r depend on.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }

@@ -65,12 +65,4 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
   }
 }
 
-// Let copies in flight land, for a producer that gives up and cannot wait on
-// a barrier of its own for them.
-__device__ __forceinline__ void settle(uint64_t ns) {
-  const uint64_t t0 = global_timer_ns();
-  while (global_timer_ns() - t0 < ns) {
-  }
-}
-
 }  // namespace moe
