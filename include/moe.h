@@ -468,7 +468,8 @@ int moe_forward_noalloc_status(void* stream);
  * negative inv_perm entry is another shard's assignment.  Rows have H elements
  * of `dtype`; any H >= 1 and any alignment of the element type (16-byte rows
  * and buffers move 16 bytes at a time).  T == 0 does nothing.  Results do not
- * depend on the schedule.  Skipped when *dev_status != 0 (it may be NULL).
+ * depend on the schedule.  Skipped when *dev_status != 0 (it may be NULL): give
+ * the word moe_align reports in, as the lists are unspecified after an error.
  *
  * moe_permute_tokens: x_sorted[inv_perm[i]] = x[i / K]; rows of padding slots
  * (sorted_ids[s] >= T*K) are set to zero, so x_sorted (cap, H) is written

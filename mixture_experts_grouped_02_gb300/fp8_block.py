@@ -107,9 +107,15 @@ def forward_fp8_block(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, b
     With num_experts given, the weights are those of the shard [expert_base,
     expert_base + L) and out is its share of the layer output.  block_m: rows
     per align block, by default 16 while the experts receive at most 16 rows
-    on average and 128 above."""
+    on average and 128 above.  dev_status: an int32 status word of the
+    caller's, zero at the start (one is made otherwise): an expert id out of
+    range is reported there, the later steps then do nothing and out is left
+    unspecified."""
     from . import align
     T, H = x.shape
+    if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids: expected (T, K) int32, got {tuple(topk_ids.shape)} "
+                         f"{topk_ids.dtype}")
     L, I = w13.shape[0], w13.shape[1] // 2
     K = topk_ids.shape[1]
     E = L if num_experts is None else num_experts
@@ -121,6 +127,8 @@ def forward_fp8_block(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, b
             out = torch.empty((T, H), dtype=x.dtype, device=x.device)
         if T == 0:
             return out
+        if dev_status is None:
+            dev_status = torch.zeros(1, dtype=torch.int32, device=x.device)
         plan = align(topk_ids, E, block_m, dev_status, None, expert_base,
                      0 if num_experts is None else L)
         xq, xs = quantize_fp8_block(x)

@@ -11,6 +11,9 @@ in 64 bits.  Tolerances, derived before any run:
    |terms| of the exact one, and the output, rounded once, lies between the
    output type's roundings of (exact - d) and (exact + d).
 """
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -398,6 +401,39 @@ def test_expert_ffn(T, E, K):
     side.synchronize()
     assert torch.equal(again, got)
     assert moe.forward_fp8_block(x[:0], ids[:0], tw[:0], w13, s13, w2, s2).shape == (0, H)
+
+
+def test_expert_ffn_with_an_id_out_of_range():
+    """Reported in the status word; the lists are unspecified then, so no later
+    step may read them."""
+    T, E, K, H, I = 20, 4, 2, 256, 128
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    ids = _ids(T, K, E, 1, False).cuda()
+    ids[7, 1] = E
+    tw = torch.full((T, K), 0.5, device="cuda")
+    args = (_codes((E, 2 * I, H), 3), _scales((E, 2, 2), 4), _codes((E, H, I), 5),
+            _scales((E, 2, 1), 6))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.forward_fp8_block(x, ids, tw, *args, dev_status=status)
+    assert moe.moe_get_device_status(status) == _abi.MOE_ERR_DEVICE_BAD_ID
+    moe.forward_fp8_block(x, ids, tw, *args)  # with a status word of its own
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        moe.forward_fp8_block(x, ids.long(), tw, *args)
+
+
+def test_example():
+    """The example runs, its fp8 layer is near the bf16 one (the bound of
+    test_expert_ffn, doubled for bf16's own rounding) and its loss falls."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "fp8_expert_layer.py")
+    spec = importlib.util.spec_from_file_location("fp8_expert_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    distances, losses = example.main(["--hidden", "512", "--inter", "256", "--experts", "16",
+                                      "--topk", "4", "--tokens", "1", "40", "300"])
+    assert max(distances) <= 0.12
+    assert losses[-1] < losses[0]
 
 
 def test_skipped_when_the_status_is_set():
