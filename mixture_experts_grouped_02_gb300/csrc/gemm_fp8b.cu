@@ -35,15 +35,18 @@
 //    4 and one half of the columns.  A warp whose 32 rows are all padding only
 //    keeps the barriers.
 //
-// 8192 x 4096 x 7168: 203-217 us (clocks between 1.6 and 1.9 GHz), 2.2-2.4
-// PFLOP/s; 380,000 clocks, about 820 per stage of two scale blocks inside a
-// tile, of which the MMAs need 512 at the full rate, and 3000 more per tile
-// for its output.  The issuing thread finds every stage and buffer ready, and
-// a second one made it 414,000, 16 epilogue warps instead of 8 nothing: what is
-// left is the 128 KB a stage moves through shared memory, copies in and
-// operands out (about 160 bytes a clock).  CTA pairs (256 rows x 128 weight
-// rows, cta_group::2) move 96 KB, but took 372,000 to 437,000 clocks: a buffer
-// comes back 1060 clocks after its last MMA there, and two buffers fill TMEM.
+// 8192 x 4096 x 7168: 205 us at 1.9 GHz, 227 in a loop of seconds under the
+// power cap (2.35 and 2.12 PFLOP/s); 380,000 clocks, about 820 per stage of two
+// scale blocks inside a tile, of which the MMAs need 512 at the full rate, and
+// 3000 more per tile for its output.  The issuing thread finds every stage and
+// buffer ready; a second one made it 414,000, 16 epilogue warps instead of 8 and
+// MMAs of the two blocks in turn changed nothing.  What is left is the MMAs
+// themselves: about 45 clocks and half a clock per column each (75, 105 and 165
+// for N = 64, 128 and 256), and sums of 256 columns do not fit the epilogue's
+// registers.  CTA pairs (256 rows x 128 weight rows, cta_group::2, 83 clocks an
+// MMA) took 372,000 to 437,000 clocks with small changes elsewhere in the
+// kernel, at best 216 us under the cap: a buffer comes back 1060 clocks after
+// its last MMA there, and two buffers fill TMEM.
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
 // up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
