@@ -555,7 +555,9 @@ int moe_test_gemm_wait_timeout(const moe_problem_t* p, int gemm, const void* a_r
 
 /* moe_gemm_fp8_block (M >= 1) in a given form of its kernel (gemm_fp8b.cu): 0
  * and 1 one CTA per tile of 64 and 128 weight rows, 2 to 4 the K range split
- * over clusters of 2, 4 and 8 CTAs; moe_gemm_fp8_block chooses by the sizes.  wait_limit_ns 0 computes the product; 1 ms to 2 s runs the
+ * over clusters of 2, 4 and 8 CTAs, 5 (gemm_fp8b_rows.cu; M <= 8, and no wait
+ * limit, as it has no waits) 16 weight rows per CTA; moe_gemm_fp8_block chooses
+ * by the sizes.  wait_limit_ns 0 computes the product; 1 ms to 2 s runs the
  * failure path as above (no copies, MOE_ERR_TIMEOUT in *dev_status, out not
  * written).  For tests. */
 int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,

@@ -268,6 +268,10 @@ struct Fp8bMaps {
 };
 cudaError_t launch_fp8b_gemm(const Fp8bArgs& a, const Fp8bForm& f, const Fp8bMaps& maps,
                              cudaStream_t s);
+// The plain product for at most kRowsMax rows of a (gemm_fp8b_rows.cu).
+constexpr int kRowsMax = 8;
+cudaError_t launch_fp8b_rows(const Fp8bArgs& a, const uint8_t* x, const uint8_t* w, int sms,
+                             cudaStream_t s);
 
 // Host helpers of moe_abi.cu: the current device's SM count, and the tensor
 // map of a row-major byte tensor (16-byte aligned, inner a multiple of 16)

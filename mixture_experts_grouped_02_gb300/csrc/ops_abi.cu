@@ -62,7 +62,7 @@ Fp8bHeld held_clusters() {
   return held[dev];
 }
 
-// `force`: null, or the form to use instead of fp8b_form's choice.
+// `force`: null, or the form to use instead of the choice by the sizes.
 int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int out_dtype,
              cudaStream_t s, const Fp8bForm* force = nullptr) {
   const int es = elem_bytes(out_dtype);
@@ -78,6 +78,14 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
   // tile indexes are 32-bit
   if (static_cast<long long>(a.max_blocks) * a.subs * ((a.N + 63) / 64) > 0x3fffffffll)
     return MOE_ERR_UNSUPPORTED;
+  // Few rows: the kernel for them, as long as latency counts.  From 64 MB of
+  // weights on both stream at HBM's rate and the tiles of the other one read a
+  // fewer times (us, 8 rows of 16384 x 7168: 28.6 and 23.7; 1 row of 16384 x
+  // 4096: 16.7 and 16.0; 8 rows of 4096 x 7168: 8.1 and 10.8).
+  const bool few = a.block_info == nullptr && a.M <= kRowsMax &&
+                   static_cast<long long>(a.N) * a.K <= (64ll << 20);
+  if (force != nullptr ? force->bn == 16 : few)
+    return cuda_status(launch_fp8b_rows(a, x, w, device_sm_count(), s));
   const Fp8bForm f = force != nullptr ? *force : fp8b_form(a, device_sm_count(), held_clusters());
   Fp8bMaps maps;
   int rc = make_byte_map(&maps.a, x, a.K, rows, 128, 128);
@@ -220,14 +228,17 @@ int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_
                             void* stream) {
   const int rc = check_gemm(1, N, K, out_dtype);
   if (rc != MOE_OK) return rc;
-  if (M <= 0 || form < 0 || form > 4) return MOE_ERR_INVALID_ARG;
+  if (M <= 0 || form < 0 || form > 5) return MOE_ERR_INVALID_ARG;
+  // the form without pipelines has no waits, and takes few rows
+  if (form == 5 && (M > kRowsMax || wait_limit_ns != 0)) return MOE_ERR_UNSUPPORTED;
   if (wait_limit_ns != 0 && (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull))
     return MOE_ERR_INVALID_ARG;
   Fp8bArgs g = plain_args(a_scale, w_scale, M, N, K, out, dev_status);
   g.timeout_ns = wait_limit_ns;
   g.starve = wait_limit_ns != 0;
   // {weight rows of a tile, mode, splits} of forms 0 to 4
-  static const int kForms[5][3] = {{64, 0, 1}, {128, 0, 1}, {64, 1, 2}, {64, 1, 4}, {64, 1, 8}};
+  static const int kForms[6][3] = {{64, 0, 1}, {128, 0, 1}, {64, 1, 2},
+                                   {64, 1, 4}, {64, 1, 8},  {16, 0, 1}};
   Fp8bForm f;
   f.bn = kForms[form][0];
   f.mode = kForms[form][1];
@@ -235,7 +246,7 @@ int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_
   const long long tiles = static_cast<long long>(g.max_blocks) * ((N + f.bn - 1) / f.bn);
   if (tiles * f.splits > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
-  f.grid = static_cast<int>(form >= 2 ? tiles * f.splits : tiles < sms ? tiles : sms);
+  f.grid = static_cast<int>(f.splits > 1 ? tiles * f.splits : tiles < sms ? tiles : sms);
   return run_gemm(g, a, M, w, out_dtype, as_stream(stream), &f);
 }
 

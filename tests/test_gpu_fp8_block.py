@@ -161,6 +161,23 @@ def test_gemm(M, N, K, dtype):
     assert bool((guard[0] == 777).all()) and bool((guard[-1] == 777).all())
 
 
+@pytest.mark.parametrize("M", range(1, 9))
+@pytest.mark.parametrize("N,K", [(1, 16), (17, 144), (520, 2064), (2500, 528), (6000, 7168)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gemm_of_few_rows(M, N, K, dtype):
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    guard = torch.full((M + 2, N), 777.0, dtype=dtype, device="cuda")
+    out = guard[1:-1]
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, moe.dtype_code(dtype), 5)
+    _close(out, _dequant(a, sa), _dequant(w, sw, N), dtype)
+    assert bool((guard[0] == 777).all()) and bool((guard[-1] == 777).all())
+    with pytest.raises(moe.MoEError):  # nine rows
+        _abi.moe_test_gemm_fp8_block(_codes((9, K), 1), _scales((9, _nblk(K)), 3), w, sw, 9, N, K,
+                                     torch.empty((9, N), dtype=dtype, device="cuda"),
+                                     moe.dtype_code(dtype), 5)
+
+
 @pytest.mark.parametrize("form", range(5))
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (5, 136, 400), (40, 200, 1168), (129, 520, 2064),
                                    (300, 257, 640), (2100, 392, 144)])
@@ -178,7 +195,7 @@ def test_gemm_in_every_form(form, M, N, K, dtype):
 # sizes on the sides of the choice between the forms: 128 and 64 weight rows to
 # a CTA, a split K
 @pytest.mark.parametrize("M,N,K", [(1300, 2000, 400), (100, 12800, 256), (2, 64, 7168),
-                                   (257, 576, 4096), (20000, 128, 272)])
+                                   (257, 576, 4096), (20000, 128, 272), (8, 9000, 7168), (8, 9600, 7168)])
 def test_gemm_across_the_choice_of_form(M, N, K):
     a, w = _codes((M, K), 1), _codes((N, K), 2)
     sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
