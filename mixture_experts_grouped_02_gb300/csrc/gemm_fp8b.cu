@@ -95,6 +95,7 @@ struct Cfg {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
   static constexpr int kCols = BN_ / 2;  // columns of an epilogue thread
+  static constexpr int kPartPitch = BN_ + 4;  // kSplit: floats of a row of partial sums
   static constexpr int kOutBytes = kEpiWarps * 2048;  // see store_rows
   static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
 };
@@ -279,6 +280,33 @@ __device__ __forceinline__ void store_rows(const Fp8bArgs& a, long long row0, in
                        __float_as_uint(v[3]));
       }
       flush(c);
+    }
+  }
+}
+
+// Up to four consecutive elements of a row of out, the first `n` of them.
+__device__ __forceinline__ void store4(const Fp8bArgs& a, long long o, int n, const float4& v) {
+  if (a.out_bf16) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + o;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    if (a.wide_out) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                  *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      out[0] = lo.x;
+      if (n > 1) out[1] = lo.y;
+      if (n > 2) out[2] = hi.x;
+      if (n > 3) out[3] = hi.y;
+    }
+  } else {
+    float* out = static_cast<float*>(a.out) + o;
+    if (a.wide_out) {
+      *reinterpret_cast<float4*>(out) = v;
+    } else {
+      out[0] = v.x;
+      if (n > 1) out[1] = v.y;
+      if (n > 2) out[2] = v.z;
+      if (n > 3) out[3] = v.w;
     }
   }
 }
@@ -641,12 +669,18 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         }
       }
       if constexpr (MODE == kSplit) {
-        // partial sums over the stages (all read by now), a row's BN + 1
+        // partial sums over the stages (all read by now), a row's kPartPitch
         // floats apart so that neither side of the exchange meets a bank twice
-        float* part = reinterpret_cast<float*>(smem_gen) + local * (BN + 1) + col_in_tile;
+        float4* part = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem_gen) +
+                                                 local * C::kPartPitch + col_in_tile);
         if (live && local < r.valid) {
 #pragma unroll
-          for (int i = 0; i < C::kCols / 2; ++i) unpack2(acc[i], part[2 * i], part[2 * i + 1]);
+          for (int i = 0; i < C::kCols / 4; ++i) {
+            float4 v;
+            unpack2(acc[2 * i], v.x, v.y);
+            unpack2(acc[2 * i + 1], v.z, v.w);
+            part[i] = v;
+          }
         }
       } else {
         if (live && !s_abort)
@@ -661,25 +695,27 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   if constexpr (MODE != kSingle) cluster_sync();
   if constexpr (MODE == kSplit) {
     // the cluster's tile: each CTA adds up and stores 64 / splits of its
-    // columns, the partial sums in rank order
+    // columns, the partial sums in rank order, four columns to a thread
     if (first < total && !s_abort) {
       const Tile t = order(first);
       const RowBlock r = row_block(a, t.mb);
-      const int span = BN / a.splits;
-      const int c0 = static_cast<int>(rank) * span;
-      for (int i = threadIdx.x; i < span * r.valid; i += blockDim.x) {
-        const int c = c0 + i % span, m = i / span;
+      const int lg = __ffs(BN / 4 / a.splits) - 1;  // splits is 2, 4 or 8
+      const int c0 = static_cast<int>(rank) * (BN / a.splits);
+      for (int i = threadIdx.x; i < r.valid << lg; i += blockDim.x) {
+        const int c = c0 + 4 * (i & ((1 << lg) - 1)), m = i >> lg;
         const int col = t.nt * BN + c;
         if (col >= a.N) continue;
-        float sum = 0.0f;
-        for (int p = 0; p < a.splits; ++p)
-          sum += __uint_as_float(
-              ld_shared_cluster_u32(mapa_shared(smemA, p) + 4u * (m * (BN + 1) + c)));
-        const long long o = static_cast<long long>(r.r0 + m) * a.N + col;
-        if (a.out_bf16)
-          static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(sum);
-        else
-          static_cast<float*>(a.out)[o] = sum;
+        const uint32_t at = smemA + 4u * (m * C::kPartPitch + c);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = 0; p < a.splits; p += 2) {
+          const float4 u = ld_shared_cluster_f4(mapa_shared(at, p));
+          const float4 v = ld_shared_cluster_f4(mapa_shared(at, p + 1));
+          sum.x = (sum.x + u.x) + v.x;
+          sum.y = (sum.y + u.y) + v.y;
+          sum.z = (sum.z + u.z) + v.z;
+          sum.w = (sum.w + u.w) + v.w;
+        }
+        store4(a, static_cast<long long>(r.r0 + m) * a.N + col, a.N - col, sum);
       }
     }
     cluster_sync();  // the peers have read this CTA's shared memory
@@ -778,15 +814,16 @@ Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
     f.bn = 64;
     f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n64));
     // Splitting K by s, where all the clusters are resident at once: 0.29 us
-    // for every stage a CTA has less, against 2.5 us of cluster launch,
-    // barriers and joining and 0.06 us per row a CTA joins (1 x 576 x 7168:
-    // 11.2 us whole, 9.3, 7.4 and 6.8 by 2, 4 and 8; 16 x 2880 x 2880: 6.9
-    // whole, 8.5 by 2; 128 x 4096 x 7168: 13.3 whole, 15.4 by 2).
+    // for every stage a CTA has less, against 2 us of cluster launch and
+    // barriers and 2.2 ns per row and partial sum to exchange them (16 x 576 x
+    // 7168: 11.2 us whole, 9.1, 7.4 and 6.7 by 2, 4 and 8; 128 x 576 x 7168:
+    // 11.7, 10.2, 8.8 and 9.1; 128 x 4096 x 7168: 13.1 whole, 11.5 by 2; 16 x
+    // 2880 x 2880: 6.8 whole, 7.2 by 2; 333 x 1024 x 4096: 8.8 and 9.0).
     const int stages = (a.k_tiles + 1) / 2;
     const double rows = a.block_info != nullptr ? std::min(a.block_m, 128) : std::min(a.M, 128);
     double best = 0.0;
     for (int i = 0, s = 2; i < 3; ++i, s *= 2) {
-      const double gain = 0.29 * (stages - div_up(stages, s)) - 2.5 - 0.06 * rows / s;
+      const double gain = 0.29 * (stages - div_up(stages, s)) - 2.0 - 0.0022 * rows * s;
       if (max_blocks * n64 <= held.split[i] && gain > best) {
         best = gain;
         f.mode = kSplit;

@@ -116,7 +116,7 @@ def forward_fp8_block(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, b
     if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError(f"topk_ids: expected (T, K) int32, got {tuple(topk_ids.shape)} "
                          f"{topk_ids.dtype}")
-    L, I = w13.shape[0], w13.shape[1] // 2
+    L = w13.shape[0]
     K = topk_ids.shape[1]
     E = L if num_experts is None else num_experts
     if block_m is None:
