@@ -35,15 +35,18 @@
 //    4 and one half of the columns.  A warp whose 32 rows are all padding only
 //    keeps the barriers.
 //
-// 8192 x 4096 x 7168: 205 us at 1.9 GHz, 227 in a loop of seconds under the
-// power cap (2.35 and 2.12 PFLOP/s); 380,000 clocks, about 820 per stage of two
+// 8192 x 4096 x 7168: 205 us at 1.85 GHz, 227 in a loop of seconds under the
+// power cap (2.35 and 2.12 PFLOP/s); 378,000 clocks, about 820 per stage of two
 // scale blocks inside a tile, of which the MMAs need 512 at the full rate, and
 // 3000 more per tile for its output.  The issuing thread finds every stage and
 // buffer ready; a second one made it 414,000, 16 epilogue warps instead of 8 and
 // MMAs of the two blocks in turn changed nothing.  What is left is the MMAs
 // themselves: about 45 clocks and half a clock per column each (75, 105 and 165
 // for N = 64, 128 and 256), and sums of 256 columns do not fit the epilogue's
-// registers.  CTA pairs (256 rows x 128 weight rows, cta_group::2, 83 clocks an
+// registers (with 16 epilogue warps of 64 columns 1,030,000 clocks, as they
+// spill).  Loading a quarter of A's bytes would save 3 %, so the loads bound
+// little; L2 copies of the weights ahead of the loads cost 3 %, and an output
+// stored by TMA as much time as one stored by the warps (384,000).  CTA pairs (256 rows x 128 weight rows, cta_group::2, 83 clocks an
 // MMA) took 372,000 to 437,000 clocks with small changes elsewhere in the
 // kernel, at best 216 us under the cap: a buffer comes back 1060 clocks after
 // its last MMA there, and two buffers fill TMEM.
@@ -749,7 +752,10 @@ cudaError_t launch(Fp8bArgs a, const Fp8bForm& f, const Fp8bMaps& maps, cudaStre
   cudaError_t err = prepare_kernel<BN, MODE>();
   if (err != cudaSuccess) return err;
   a.n_tiles = (a.N + BN - 1) / BN;
-  a.band = std::min(a.n_tiles, 8);
+  // Tiles in flight together: 152 / 16 row blocks by 16 weight tiles.  In bands
+  // of 4, 8, 16 and 32 weight tiles 8192 rows over 32 experts of 4096 x 7168 took
+  // 302, 282, 276 and 278 us, 8192 x 4096 x 7168 210, 208, 205 and 206.
+  a.band = std::min(a.n_tiles, 16);
   a.splits = f.splits;
   cudaLaunchAttribute attr[2];
   const unsigned cluster = MODE == kSplit ? f.splits : 1;
