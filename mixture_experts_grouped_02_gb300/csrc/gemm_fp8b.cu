@@ -36,20 +36,22 @@
 //    keeps the barriers.
 //
 // 8192 x 4096 x 7168: 205 us at 1.85 GHz, 227 in a loop of seconds under the
-// power cap (2.35 and 2.12 PFLOP/s); 378,000 clocks, about 820 per stage of two
-// scale blocks inside a tile, of which the MMAs need 512 at the full rate, and
-// 3000 more per tile for its output.  The issuing thread finds every stage and
-// buffer ready; a second one made it 414,000, 16 epilogue warps instead of 8 and
-// MMAs of the two blocks in turn changed nothing.  What is left is the MMAs
-// themselves: about 45 clocks and half a clock per column each (75, 105 and 165
-// for N = 64, 128 and 256), and sums of 256 columns do not fit the epilogue's
-// registers (with 16 epilogue warps of 64 columns 1,030,000 clocks, as they
-// spill).  Loading a quarter of A's bytes would save 3 %, so the loads bound
-// little; L2 copies of the weights ahead of the loads cost 3 %, and an output
-// stored by TMA as much time as one stored by the warps (384,000).  CTA pairs (256 rows x 128 weight rows, cta_group::2, 83 clocks an
-// MMA) took 372,000 to 437,000 clocks with small changes elsewhere in the
-// kernel, at best 216 us under the cap: a buffer comes back 1060 clocks after
-// its last MMA there, and two buffers fill TMEM.
+// power cap (2.35 and 2.12 PFLOP/s); 378,000 clocks, about 860 per stage of two
+// scale blocks inside a tile and 2500 more per tile for its output.  What
+// bounds a stage is shared memory: its MMAs need 512 clocks at the full rate and
+// take them when the operands stay in place (all SMs busy), reading 64 KB at
+// 128 bytes a clock; TMA's writes of the next 64 KB, at 256 bytes a clock, add
+// to that.  The sum, 768, is what a stage takes when the epilogue only hands the
+// buffers back (758; with 64 weight rows 576 and 560, with a quarter of A's
+// bytes 672 and 676).  Fewer bytes per product need wider tiles: sums of 256
+// columns do not fit the epilogue's registers (with 16 epilogue warps of 64
+// columns 1,030,000 clocks, as they spill), and CTA pairs (256 rows x 128
+// weight rows, cta_group::2) took 372,000 to 437,000 clocks with small changes
+// elsewhere in the kernel, at best 216 us under the cap: a buffer comes back
+// 1060 clocks after its last MMA there, and two buffers fill TMEM.  No gain
+// from: a second issuing thread (414,000), 16 epilogue warps (420,000), buffers
+// given back by scale block (384,000), four buffers of 64 columns, L2 copies of
+// the weights ahead of the loads (393,000), outputs stored by TMA (384,000).
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
 // up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
