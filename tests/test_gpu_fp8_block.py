@@ -514,3 +514,31 @@ def test_checked_build_skips_blocks_outside_the_weights():
                                         torch.cuda.current_stream().cuda_stream) == _abi.MOE_OK
     assert int(st.item()) == _abi.MOE_ERR_BOUNDS
     assert bool((out == 7).all())
+
+
+# a multiple of four scale blocks to a row (loaded four at a time where rows
+# start on 16 bytes)
+@pytest.mark.parametrize("form", range(6))
+@pytest.mark.parametrize("off", [0, 1, 2])
+@pytest.mark.parametrize("M,N,K", [(7, 264, 1536), (8, 200, 3584), (1, 64, 512)])
+def test_gemm_scales_on_any_alignment(form, off, M, N, K):
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sw = _scales((_nblk(N), _nblk(K)), 4)
+    sa = torch.empty(M * _nblk(K) + off, device="cuda")[off:].view(M, _nblk(K))
+    sa.copy_(_scales((M, _nblk(K)), 3))
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form)
+    _close(out, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(130, 392, 2048), (300, 1000, 4608)])
+def test_gemm_of_many_rows_with_scales_on_any_alignment(off, M, N, K):
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sw = _scales((_nblk(N), _nblk(K)), 4)
+    sa = torch.empty(M * _nblk(K) + off, device="cuda")[off:].view(M, _nblk(K))
+    sa.copy_(_scales((M, _nblk(K)), 3))
+    for form in range(5):
+        out = torch.empty((M, N), dtype=torch.float32, device="cuda")
+        _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_F32, form)
+        _close(out, _dequant(a, sa), _dequant(w, sw, N), torch.float32)
