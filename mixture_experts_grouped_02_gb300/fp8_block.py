@@ -78,8 +78,8 @@ def gemm_fp8_block(a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, d
 def grouped_gemm_fp8_block(a, a_scale, w, w_scale, plan, block_m=128, out=None,
                            out_dtype=torch.bfloat16, dev_status=None, stream=None):
     """The sorted rows a (cap, K) times their experts' w (E, N, K) transposed,
-    (cap, N); `plan` and `block_m` as given to :func:`align`.  Rows of padding
-    slots of out are not written."""
+    (cap, N); `plan` and `block_m` as given to :func:`align`, over at most
+    the E experts that w holds.  Rows of padding slots of out are not written."""
     rows, K = a.shape
     E, N = w.shape[0], w.shape[1]
     cap = _lists(plan)[2]
@@ -89,6 +89,11 @@ def grouped_gemm_fp8_block(a, a_scale, w, w_scale, plan, block_m=128, out=None,
                          f"{block_m}")
     if info.dtype != torch.int32 or num.dtype != torch.int32:
         raise ValueError("block_info and num_blocks are int32 tensors")
+    # block_info's expert ids index w and w_scale: a list over other experts
+    # would be read past their end
+    counts = plan.get("counts")
+    if counts is not None and counts.numel() > E:
+        raise ValueError(f"the plan is over {counts.numel()} experts, w holds {E}")
     _codes(a, (cap, K), "a")
     _codes(w, (E, N, K), "w")
     _scales(a_scale, (cap, _nblk(K)), "a_scale")
