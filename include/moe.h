@@ -467,7 +467,8 @@ int moe_forward_noalloc_status(void* stream);
  * i = t*K + k; inv_perm (T*K) and sorted_ids (cap) as moe_align writes them; a
  * negative inv_perm entry is another shard's assignment.  Rows have H elements
  * of `dtype`; any H >= 1 and any alignment of the element type (16-byte rows
- * and buffers move 16 bytes at a time).  T == 0 does nothing.  Results do not
+ * and buffers move 16 bytes at a time).  Pointers off their element type's
+ * alignment are refused (MOE_ERR_INVALID_ARG), here and in the calls below.  T == 0 does nothing.  Results do not
  * depend on the schedule.  Skipped when *dev_status != 0 (it may be NULL): give
  * the word moe_align reports in, as the lists are unspecified after an error.
  *

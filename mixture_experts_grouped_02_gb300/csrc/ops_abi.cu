@@ -26,6 +26,12 @@ int elem_bytes(int dtype, bool codes = false) {
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+// int32 and fp32 arguments, which the kernels access as 4-byte words.
+template <typename... P>
+bool words(const P*... p) {
+  return (aligned(p, 4) && ...);
+}
+
 // Sizes shared by the four permutation entry points; cap is an int32 slot
 // count in the lists.
 int check_list(int T, int H, int K, size_t cap, int es) {
@@ -67,7 +73,7 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
              cudaStream_t s, const Fp8bForm* force = nullptr) {
   const int es = elem_bytes(out_dtype);
   if (!x || !a.a_scale || !w || !a.w_scale || !a.out || !aligned(x, 16) || !aligned(w, 16) ||
-      !aligned(a.a_scale, 4) || !aligned(a.w_scale, 4) || !aligned(a.out, es))
+      !words(a.a_scale, a.w_scale, a.num_blocks, a.status) || !aligned(a.out, es))
     return MOE_ERR_INVALID_ARG;
   a.k_tiles = (a.K + 127) / 128;
   a.n_scales = (a.N + 127) / 128;
@@ -124,7 +130,8 @@ int moe_permute_tokens(const void* x, int dtype, int T, int H, int K, const int3
   const int es = elem_bytes(dtype, true);
   const int rc = check_list(T, H, K, cap, es);
   if (rc != MOE_OK || T == 0) return rc;
-  if (!x || !inv_perm || !sorted_ids || !x_sorted || !aligned(x, es) || !aligned(x_sorted, es))
+  if (!x || !inv_perm || !sorted_ids || !x_sorted || !aligned(x, es) || !aligned(x_sorted, es) ||
+      !words(inv_perm, sorted_ids, dev_status))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_permute(x, T, static_cast<long long>(H) * es, K, inv_perm, sorted_ids,
                                     static_cast<long long>(cap), x_sorted, dev_status,
@@ -137,7 +144,8 @@ int moe_permute_tokens_backward(const void* grad_sorted, int dtype, int T, int H
   const int es = elem_bytes(dtype);
   const int rc = check_list(T, H, K, cap, es);
   if (rc != MOE_OK || T == 0) return rc;
-  if (!grad_sorted || !inv_perm || !grad_x || !aligned(grad_sorted, es) || !aligned(grad_x, es))
+  if (!grad_sorted || !inv_perm || !grad_x || !aligned(grad_sorted, es) || !aligned(grad_x, es) ||
+      !words(inv_perm, dev_status))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_unpermute(grad_sorted, dtype, nullptr, T, K, H, inv_perm,
                                       static_cast<long long>(cap), grad_x, dev_status,
@@ -150,7 +158,8 @@ int moe_unpermute_tokens(const void* y, int dtype, int T, int H, int K, const fl
   const int es = elem_bytes(dtype);
   const int rc = check_list(T, H, K, cap, es);
   if (rc != MOE_OK || T == 0) return rc;
-  if (!y || !topk_weights || !inv_perm || !out || !aligned(y, es) || !aligned(out, es))
+  if (!y || !topk_weights || !inv_perm || !out || !aligned(y, es) || !aligned(out, es) ||
+      !words(topk_weights, inv_perm, dev_status))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_unpermute(y, dtype, topk_weights, T, K, H, inv_perm,
                                       static_cast<long long>(cap), out, dev_status,
@@ -165,7 +174,8 @@ int moe_unpermute_tokens_backward(const void* grad_out, const void* y, int dtype
   const int rc = check_list(T, H, K, cap, es);
   if (rc != MOE_OK || T == 0) return rc;
   if (!grad_out || !y || !topk_weights || !inv_perm || !sorted_ids || !grad_y || !grad_weights ||
-      !aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_y, es))
+      !aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_y, es) ||
+      !words(topk_weights, inv_perm, sorted_ids, grad_weights, dev_status))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_unpermute_backward(
       grad_out, y, dtype, topk_weights, T, K, H, inv_perm, sorted_ids,
@@ -179,7 +189,7 @@ int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, 
   if (T == 0) return MOE_OK;
   // blocks are counted in 32 bits, and so are their CTAs
   if (static_cast<long long>(T) * ((H + 127ll) / 128) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
-  if (!x || !xq || !scale || !aligned(x, es)) return MOE_ERR_INVALID_ARG;
+  if (!x || !xq || !scale || !aligned(x, es) || !words(scale)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       launch_quantize_block(x, x_dtype, T, H, gated, xq, scale, as_stream(stream)));
 }

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import mixture_experts_grouped_02_gb300 as moe
+from mixture_experts_grouped_02_gb300 import _abi
 
 
 def _plan(cap, block_m, experts):
@@ -23,3 +24,44 @@ def test_grouped_product_refuses_a_plan_over_more_experts(experts):
     with pytest.raises(ValueError, match=f"over {experts} experts, w holds 3"):
         moe.grouped_gemm_fp8_block(a, torch.ones((cap, 1)), w, torch.ones((E, 1, 1)),
                                    _plan(cap, 16, experts), 16)
+
+
+# Pointers of the C entry points, none of which is followed: the calls below
+# are refused by their argument checks.
+A = 1 << 20
+PERMUTE = dict(x=A, dtype=_abi.MOE_BF16, T=4, H=64, K=2, inv_perm=A, sorted_ids=A, cap=8,
+               x_sorted=A, dev_status=A, stream=0)
+PERMUTE_BACKWARD = dict(grad_sorted=A, dtype=_abi.MOE_BF16, T=4, H=64, K=2, inv_perm=A, cap=8,
+                        grad_x=A, dev_status=A, stream=0)
+UNPERMUTE = dict(y=A, dtype=_abi.MOE_BF16, T=4, H=64, K=2, topk_weights=A, inv_perm=A, cap=8,
+                 out=A, dev_status=A, stream=0)
+UNPERMUTE_BACKWARD = dict(grad_out=A, y=A, dtype=_abi.MOE_BF16, T=4, H=64, K=2, topk_weights=A,
+                          inv_perm=A, sorted_ids=A, cap=8, grad_y=A, grad_weights=A, dev_status=A,
+                          stream=0)
+QUANTIZE = dict(x=A, x_dtype=_abi.MOE_BF16, T=4, H=64, gated=0, xq=A, scale=A, stream=0)
+GEMM = dict(a=A, a_scale=A, w=A, w_scale=A, M=4, N=64, K=128, out=A, out_dtype=_abi.MOE_BF16,
+            dev_status=A, stream=0)
+GROUPED = dict(a=A, a_scale=A, w=A, w_scale=A, E=2, N=64, K=128, cap=32, block_m=16,
+               block_info=A, num_blocks=A, out=A, out_dtype=_abi.MOE_BF16, dev_status=A, stream=0)
+CALLS = dict(moe_permute_tokens=PERMUTE, moe_permute_tokens_backward=PERMUTE_BACKWARD,
+             moe_unpermute_tokens=UNPERMUTE, moe_unpermute_tokens_backward=UNPERMUTE_BACKWARD,
+             moe_quantize_fp8_block=QUANTIZE, moe_gemm_fp8_block=GEMM,
+             moe_grouped_gemm_fp8_block=GROUPED)
+
+
+def _refused(name, **changed):
+    with pytest.raises(moe.MoEError) as e:
+        getattr(_abi, name)(**{**CALLS[name], **changed})
+    return e.value.status
+
+
+WORDS = ("inv_perm", "sorted_ids", "topk_weights", "grad_weights", "scale", "a_scale", "w_scale",
+         "block_info", "num_blocks", "dev_status")
+
+
+@pytest.mark.parametrize("name,arg", [(n, a) for n, c in CALLS.items() for a in c
+                                      if c[a] == A and a not in ("xq",)])
+def test_pointers_off_their_alignment_are_refused(name, arg):
+    """One byte off for every argument, two for the 4-byte words."""
+    for off in (1, 2) if arg in WORDS else (1,):
+        assert _refused(name, **{arg: A + off}) == _abi.MOE_ERR_INVALID_ARG
