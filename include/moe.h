@@ -466,11 +466,12 @@ int moe_forward_noalloc_status(void* stream);
  * their own for a caller with its own expert computation, and in training.
  * i = t*K + k; inv_perm (T*K) and sorted_ids (cap) as moe_align writes them; a
  * negative inv_perm entry is another shard's assignment.  Rows have H elements
- * of `dtype`; any H >= 1 and any alignment of the element type (16-byte rows
- * and buffers move 16 bytes at a time).  Pointers off their element type's
- * alignment are refused (MOE_ERR_INVALID_ARG), here and in the calls below.  T == 0 does nothing.  Results do not
- * depend on the schedule.  Skipped when *dev_status != 0 (it may be NULL): give
- * the word moe_align reports in, as the lists are unspecified after an error.
+ * of `dtype`; any 1 <= H < 2^31 - 4096 and any alignment of the element type
+ * (16-byte rows and buffers move 16 bytes at a time).  Pointers off their
+ * element type's alignment are refused (MOE_ERR_INVALID_ARG), here and in the
+ * calls below.  T == 0 does nothing.  Results do not depend on the schedule.
+ * Skipped when *dev_status != 0 (it may be NULL): give the word moe_align
+ * reports in, as the lists are unspecified after an error.
  *
  * moe_permute_tokens: x_sorted[inv_perm[i]] = x[i / K]; rows of padding slots
  * (sorted_ids[s] >= T*K) are set to zero, so x_sorted (cap, H) is written
@@ -506,7 +507,7 @@ int moe_unpermute_tokens_backward(const void* grad_out, const void* y, int dtype
  *   xq = e4m3_rn_satfinite(v * (448 / m)), in fp32 with IEEE rounding.
  * x (T, H) in x_dtype (MOE_BF16 or MOE_F32), v = x; with gated = 1, x (T, 2H)
  * holds gate then up and v = gate / (1 + e^-gate) * up in fp32 (fast exponential
- * and division).  xq (T, H) codes, scale (T, ceil(H/128)) fp32.  Any H >= 1.
+ * and division).  xq (T, H) codes, scale (T, ceil(H/128)) fp32.  H as above.
  * A NaN becomes a NaN code; a block with an infinity gets an infinite scale. */
 int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, uint8_t* xq,
                            float* scale, void* stream);
@@ -518,9 +519,10 @@ int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, 
  *   a (M, K) codes, a_scale (M, ceil(K/128)) fp32 as moe_quantize_fp8_block
  *   writes them; w (N, K) codes, w_scale (ceil(N/128), ceil(K/128)) fp32, one
  *   scale per 128 x 128 block (the last ones may be short); out (M, N).
- * K must be a multiple of 16 (else MOE_ERR_UNSUPPORTED); any N >= 1; M == 0
- * does nothing.  a and w 16-byte aligned.  The gradient with respect to a is the
- * same product with the transposed codes and the transposed block scales.
+ * K must be a multiple of 16 below 2^31 - 4096 (else MOE_ERR_UNSUPPORTED); any
+ * N >= 1; M == 0 does nothing.  a and w 16-byte aligned.  The gradient with
+ * respect to a is the same product with the transposed codes and the transposed
+ * block scales.
  *
  * moe_grouped_gemm_fp8_block: row s of an align block with expert e times w[e]:
  *   a (cap, K) and a_scale (cap, ceil(K/128)) in sorted order, w (E, N, K),

@@ -32,11 +32,15 @@ bool words(const P*... p) {
   return (aligned(p, 4) && ...);
 }
 
+// Columns of a row: the kernels count them in 32 bits and step past the last
+// one by up to one CTA's worth (2048).
+constexpr int kMaxColumns = 0x7fffffff - 4096;
+
 // Sizes shared by the four permutation entry points; cap is an int32 slot
 // count in the lists.
 int check_list(int T, int H, int K, size_t cap, int es) {
   if (T < 0 || H <= 0 || K <= 0 || es == 0) return MOE_ERR_INVALID_ARG;
-  if (static_cast<long long>(T) * K >= (1ll << 30) || cap > 0x7fffffffull)
+  if (static_cast<long long>(T) * K >= (1ll << 30) || cap > 0x7fffffffull || H > kMaxColumns)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -44,7 +48,7 @@ int check_list(int T, int H, int K, size_t cap, int es) {
 int check_gemm(int E, int N, int K, int out_dtype) {
   if (E <= 0 || N <= 0 || K <= 0 || elem_bytes(out_dtype) == 0) return MOE_ERR_INVALID_ARG;
   // TMA rows start on 16 bytes, and row coordinates are 32-bit
-  if (K % 16 != 0 || static_cast<long long>(E) * N >= (1ll << 31) - 256)
+  if (K % 16 != 0 || K > kMaxColumns || static_cast<long long>(E) * N >= (1ll << 31) - 256)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -188,7 +192,8 @@ int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, 
   if (T < 0 || H <= 0 || es == 0 || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   // blocks are counted in 32 bits, and so are their CTAs
-  if (static_cast<long long>(T) * ((H + 127ll) / 128) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * ((H + 127ll) / 128) >= (1ll << 31) || H > kMaxColumns)
+    return MOE_ERR_UNSUPPORTED;
   if (!x || !xq || !scale || !aligned(x, es) || !words(scale)) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       launch_quantize_block(x, x_dtype, T, H, gated, xq, scale, as_stream(stream)));

@@ -65,3 +65,12 @@ def test_pointers_off_their_alignment_are_refused(name, arg):
     """One byte off for every argument, two for the 4-byte words."""
     for off in (1, 2) if arg in WORDS else (1,):
         assert _refused(name, **{arg: A + off}) == _abi.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_rows_near_2_31_columns_are_refused(name):
+    """A CTA steps past a row's last column by up to its own width: column
+    indexes of the widest rows would not stay in 32 bits."""
+    arg = "K" if "gemm" in name else "H"
+    for n in (2 ** 31 - 16, 2 ** 31 - 2048, 2 ** 31 - 4080):
+        assert _refused(name, **{arg: n}) == _abi.MOE_ERR_UNSUPPORTED
