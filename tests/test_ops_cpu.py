@@ -74,3 +74,58 @@ def test_rows_near_2_31_columns_are_refused(name):
     arg = "K" if "gemm" in name else "H"
     for n in (2 ** 31 - 16, 2 ** 31 - 2048, 2 ** 31 - 4080):
         assert _refused(name, **{arg: n}) == _abi.MOE_ERR_UNSUPPORTED
+
+
+class _On(torch.Tensor):
+    """A CPU tensor that claims a GPU, and memory there."""
+    gpu = 0
+
+    def get_device(self):
+        return self.gpu
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def _at(gpu, *shape, dtype=torch.float32):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(_On)
+    t.gpu = gpu
+    return t
+
+
+def _device_calls(gpu, other):
+    """Every call with its first tensor on `gpu` and one later one on `other`."""
+    i32, u8 = torch.int32, torch.uint8
+
+    def plan(where):
+        return dict(sorted_ids=_at(where, 32, dtype=i32), inv_perm=_at(where, 8, dtype=i32),
+                    block_info=_at(where, 2, 4, dtype=i32), num_blocks=_at(where, 1, dtype=i32))
+
+    x, y, w = _at(gpu, 4, 64), _at(gpu, 32, 64), _at(other, 4, 2)
+    a, s = _at(gpu, 32, 128, dtype=u8), _at(gpu, 32, 1)
+    weights, ws = _at(other, 2, 48, 128, dtype=u8), _at(gpu, 2, 1, 1)
+    return [
+        lambda: moe.permute_tokens(x, plan(other)),
+        lambda: moe.permute_tokens_backward(y, plan(other), 2),
+        lambda: moe.unpermute_tokens(y, plan(gpu), w),
+        lambda: moe.unpermute_tokens_backward(x, y, plan(gpu), w),
+        lambda: moe.quantize_fp8_block(x, out=(_at(other, 4, 64, dtype=u8), _at(gpu, 4, 1))),
+        lambda: moe.gemm_fp8_block(a, s, _at(other, 48, 128, dtype=u8), _at(gpu, 1, 1)),
+        lambda: moe.grouped_gemm_fp8_block(a, s, weights, ws, plan(gpu), 16),
+        lambda: moe.forward_fp8_block(_at(gpu, 4, 128), _at(other, 4, 2, dtype=i32), w,
+                                      _at(gpu, 2, 256, 128, dtype=u8), _at(gpu, 2, 2, 1),
+                                      _at(gpu, 2, 128, 128, dtype=u8), _at(gpu, 2, 1, 1)),
+    ]
+
+
+@pytest.mark.parametrize("call", range(8))
+def test_tensors_of_other_devices_are_refused(call, monkeypatch):
+    """A launch takes the current device's kernels and stream: tensors that do
+    not share it are refused before it."""
+    monkeypatch.setattr(_abi, "_device", lambda: 0)
+    monkeypatch.setattr(_abi, "lib", lambda: pytest.fail("reached the library"))
+    with pytest.raises(ValueError, match="different devices"):
+        _device_calls(0, 1)[call]()
+    with pytest.raises(ValueError, match="the current device is cuda:0"):
+        _device_calls(1, 1)[call]()
