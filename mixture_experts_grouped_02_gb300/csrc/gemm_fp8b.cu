@@ -89,10 +89,11 @@ struct Cfg {
   static constexpr int kBufCols = kSub * BN_;
   static constexpr int kTmemCols = kBufs * kBufCols;
   // Scale slots.  Stage j takes the slot of stage j - kSlots, which has been
-  // read once the MMAs of stage j - kSlots + kBufs = j - kStages are done (they
-  // wait for the buffer of j - kSlots).  With kStages slots, the scales of a
-  // stage could be written only after the MMAs of the stage before it: 249 us
-  // instead of 217 for 8192 x 4096 x 7168.
+  // read once the MMAs of stage j - kSlots + kBufs = j - kStages are done: they
+  // wait for the buffer of j - kSlots, which every epilogue warp gives back by
+  // an arrival that releases its lanes' reads of the slot.  With kStages slots,
+  // the scales of a stage could be written only after the MMAs of the stage
+  // before it: 249 us instead of 217 for 8192 x 4096 x 7168.
   static constexpr int kSlots = kStages + kBufs;
   static constexpr int kMmaWarp = 1;
   static constexpr int kScaleWarp = 2;
@@ -606,9 +607,13 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
         __syncwarp();
         tc_fence_after_sync();
       };
+      // Gives the buffer and the scale slot back: the fence orders the TMEM
+      // loads, the warp barrier and the arrival's release the lanes' reads of
+      // s_scale, before the slot is written again.
       auto release = [&] {
         tc_fence_before_sync();
-        if (lane == 0) mbar_arrive_relaxed(smem_u32(&acce_bar[buf]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&acce_bar[buf]));
       };
       auto next_stage = [&] {
         buf ^= 1;

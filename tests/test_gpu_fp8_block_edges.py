@@ -1,0 +1,28 @@
+"""The 128-block fp8 quantiser and products where their kernels hand data from
+one warp to another, loop, or stop: against the formulas in 64 bits, with the
+bounds of test_gpu_fp8_block.py unless a test derives its own."""
+import pytest
+import torch
+
+import mixture_experts_grouped_02_gb300 as moe
+from mixture_experts_grouped_02_gb300 import _abi
+from test_gpu_fp8_block import _close, _codes, _dequant, _gen, _nblk, _scales
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("form", range(5))
+@pytest.mark.parametrize("M,N,K", [(20, 1000, 7168), (400, 1000, 4608), (2500, 1096, 2048)])
+def test_scales_change_with_every_slot(form, M, N, K):
+    """Row scales from 2^-40 to 2^40 over many stages and tiles: a scale slot
+    written before its last reader is done moves a sum by powers of two."""
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    e = torch.randint(-40, 41, (M, _nblk(K)), generator=_gen(5), device="cuda")
+    sa, sw = torch.exp2(e.float()), _scales((_nblk(N), _nblk(K)), 4)
+    outs = []
+    for _ in range(3):
+        out = torch.empty((M, N), dtype=torch.float32, device="cuda")
+        _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_F32, form)
+        outs.append(out)
+    _close(outs[0], _dequant(a, sa), _dequant(w, sw, N), torch.float32)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
