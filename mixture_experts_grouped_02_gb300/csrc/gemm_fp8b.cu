@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
       // Waits for a stage's MMAs: its products are in TMEM.  After a wait that
-      // ran out the loop goes on to its end without waiting, so that the warp
-      // stays converged; nothing is stored then.
+      // ran out the tile's loop goes on to its end without waiting, so that the
+      // warp stays converged; nothing is stored then.
       auto wait = [&] {
         mbar_wait_suspend(smem_u32(&empty_bar[stage]), phase, &s_abort, to);
         __syncwarp();
@@ -696,6 +696,10 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           }
         }
       }
+      // A wait ran out: no output, and no further tile.  One answer for the
+      // warp, whose lanes store together (another thread may raise the flag
+      // between two lanes' reads of it).
+      if (__any_sync(0xffffffffu, s_abort)) break;
       if constexpr (MODE == kSplit) {
         // partial sums over the stages (all read by now), a row's kPartPitch
         // floats apart so that neither side of the exchange meets a bank twice
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           }
         }
       } else {
-        if (live && !s_abort)
+        if (live)
           store_rows<C::kCols>(a, r.r0 + q * 32, min(32, r.valid - q * 32), col, acc,
                                out_stage + (warp - C::kFirstEpi) * 128, lane);
       }
