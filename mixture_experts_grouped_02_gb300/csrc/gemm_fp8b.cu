@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_skip;
   __shared__ volatile int s_abort;
+  __shared__ volatile int s_cluster_abort;  // kSplit: some CTA of the cluster gave up
 
   // through a shuffle, so that the compiler knows it to be the same for a warp
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   if (threadIdx.x == 0) {
     s_skip = (a.status != nullptr && *reinterpret_cast<volatile int32_t*>(a.status) != 0);
     s_abort = 0;
+    s_cluster_abort = 0;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&full_bar[i]), 2);  // the expected bytes and the scales
       mbar_init(smem_u32(&empty_bar[i]), 1);
@@ -724,11 +726,16 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (MODE != kSingle) cluster_sync();
   if constexpr (MODE == kSplit) {
+    // a CTA that gave up has no sums to add: none of its cluster stores
+    if (s_abort && threadIdx.x < a.splits)
+      st_shared_cluster_u32(
+          mapa_shared(smem_u32(const_cast<int*>(&s_cluster_abort)), threadIdx.x), 1u);
+    __syncwarp();
+    cluster_sync();
     // the cluster's tile: each CTA adds up and stores 64 / splits of its
     // columns, the partial sums in rank order, four columns to a thread
-    if (first < total && !s_abort) {
+    if (first < total && !s_cluster_abort) {
       const Tile t = order(first);
       const RowBlock r = row_block(a, t.mb);
       const int lg = __ffs(BN / 4 / a.splits) - 1;  // splits is 2, 4 or 8

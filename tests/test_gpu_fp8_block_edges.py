@@ -26,3 +26,22 @@ def test_scales_change_with_every_slot(form, M, N, K):
         outs.append(out)
     _close(outs[0], _dequant(a, sa), _dequant(w, sw, N), torch.float32)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("form", [2, 3, 4])
+@pytest.mark.parametrize("K", [128, 256, 384])
+def test_a_cluster_stores_nothing_when_one_of_its_ctas_gave_up(form, K):
+    """Of the CTAs that share so short a K some have no scale block: with no
+    copies in flight they finish, the others' waits run out.  The first ones must
+    not store what the others left in shared memory."""
+    M, N = 300, 400
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form, 2_000_000,
+                                 status)
+    assert moe.moe_get_device_status(status) == _abi.MOE_ERR_TIMEOUT
+    assert bool((out == 7).all())
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form)
+    _close(out, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
