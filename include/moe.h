@@ -562,7 +562,8 @@ int moe_test_gemm_wait_timeout(const moe_problem_t* p, int gemm, const void* a_r
  * limit, as it has no waits) 16 weight rows per CTA; moe_gemm_fp8_block chooses
  * by the sizes.  wait_limit_ns 0 computes the product; 1 ms to 2 s runs the
  * failure path as above (no copies, MOE_ERR_TIMEOUT in *dev_status, out not
- * written).  For tests. */
+ * written); with 16 added to form it holds back the scales only, so that copies
+ * are issued whose stages nobody takes.  For tests. */
 int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_t* w,
                             const float* w_scale, int M, int N, int K, void* out, int out_dtype,
                             int form, unsigned long long wait_limit_ns, int32_t* dev_status,

@@ -54,8 +54,9 @@
 // the weights ahead of the loads (393,000), outputs stored by TMA (384,000).
 //
 // Every mbarrier wait is bounded, as in the other GEMMs: a thread that gives
-// up raises the CTA's abort flag and the kernel records MOE_ERR_TIMEOUT,
-// drains and frees its TMEM.
+// up raises the CTA's abort flag, the copies and MMAs that any warp has in
+// flight drain (with a limit), and the kernel records MOE_ERR_TIMEOUT and frees
+// its TMEM.  Fp8bArgs::starve makes waits run out for tests of this path.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -396,16 +397,22 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
   const int ke = MODE == kSplit ? a.k_tiles * (static_cast<int>(rank) + 1) / a.splits : a.k_tiles;
   const uint64_t to = a.timeout_ns;
 
+  // what this thread may leave in flight (the producer's copies of stages, the
+  // issuer's MMAs) when a wait runs out in another warp
+  unsigned issued = 0;
+  bool issuer = false;
+  // the failure-path test: no copies, or no scales, so that waits run out
+  const bool copies = a.starve == kStarveNone || a.starve == kStarveScales;
+  const bool scales = a.starve == kStarveNone;
+
   // MMA columns of weight tile nt: a multiple of 16
   auto tile_cols = [&](int nt) { return min(BN, (a.N - nt * BN + 15) & ~15); };
 
   if (warp < C::kFirstEpi) {
     if (warp == 0) {
       // ----------------------------------------------------- TMA producer
-      // (a.starve, the failure-path test: no copies at all)
-      if (elect_one() && !a.starve) {
+      if (elect_one() && copies) {
         uint32_t stage = 0, phase = 0;
-        unsigned issued = 0;
         bool ok = true;
         for (int tile = first; tile < total && ok; tile += step) {
           const Tile t = order(tile);
@@ -436,11 +443,6 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
             }
           }
         }
-        if (!ok) {
-          const unsigned n0 = issued > C::kStages ? issued - C::kStages : 0;
-          for (unsigned n = n0; n < issued; ++n)
-            drain_wait(smem_u32(&full_bar[n % C::kStages]), (n / C::kStages) & 1, to / 4);
-        }
       }
     } else if (warp == C::kMmaWarp && elect_one()) {
       // ----------------------------------------------------- MMA issuer
@@ -448,6 +450,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
       const uint64_t a_desc0 = sw128_kmajor_desc(smemA), b_desc0 = sw128_kmajor_desc(smemB);
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
       bool ok = true;
+      issuer = true;
       for (int tile = first; tile < total && ok; tile += step) {
         const Tile t = order(tile);
         if (row_block(a, t.mb).valid <= 0) continue;
@@ -489,11 +492,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
           }
         }
       }
-      if (!ok) {
-        umma_commit(smem_u32(&drain_bar));
-        drain_wait(smem_u32(&drain_bar), 0, to / 4);
-      }
-    } else if (warp == C::kScaleWarp && !a.starve) {
+    } else if (warp == C::kScaleWarp && scales) {
       // ----------------------------------------------------- scales
       // A lane has four rows; the scale blocks of kGroup stages are loaded
       // together (a 32-byte sector of each row), while those of the kGroup
@@ -726,6 +725,17 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
+  if (s_abort) {
+    // no warp waits any more, and only these threads know what is under way
+    if (issuer) {
+      umma_commit(smem_u32(&drain_bar));
+      drain_wait(smem_u32(&drain_bar), 0, to / 4);
+    }
+    const unsigned n0 = issued > C::kStages ? issued - C::kStages : 0;
+    for (unsigned n = n0; n < issued; ++n)
+      drain_wait(smem_u32(&full_bar[n % C::kStages]), (n / C::kStages) & 1, to / 4);
+    __syncwarp();
+  }
   if constexpr (MODE == kSplit) {
     // a CTA that gave up has no sums to add: none of its cluster stores
     if (s_abort && threadIdx.x < a.splits)

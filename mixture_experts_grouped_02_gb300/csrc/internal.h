@@ -247,8 +247,10 @@ struct Fp8bArgs {
   int out_bf16, wide_out;      // wide_out: 16-byte stores fit every row
   int32_t* status;
   unsigned long long timeout_ns;
-  int starve;                  // failure-path test: the producer issues no copies
+  int starve;                  // failure-path test: what is held back (Fp8bStarve)
 };
+// kStarveAll: no copies and no scales; kStarveScales: copies, but no scales.
+enum Fp8bStarve { kStarveNone = 0, kStarveAll = 1, kStarveScales = 2 };
 // How a product is cut: weight rows of a tile, mode (gemm_fp8b.cu), CTAs that
 // share a tile's K range, CTAs in all.
 struct Fp8bForm {

@@ -45,3 +45,31 @@ def test_a_cluster_stores_nothing_when_one_of_its_ctas_gave_up(form, K):
     assert bool((out == 7).all())
     _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form)
     _close(out, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
+
+
+@pytest.mark.parametrize("form", range(5))
+@pytest.mark.parametrize("K", [128, 512, 1024, 7168])
+def test_waits_that_run_out_with_copies_in_flight(form, K):
+    """With the scales held back the copies are issued and no stage is taken:
+    the issuing thread gives up while the producer has either left (a K of few
+    stages) or waits as well.  The kernel drains, reports MOE_ERR_TIMEOUT, writes
+    nothing and leaves the device usable."""
+    M, N = 300, 400
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form + 16, 2_000_000,
+                                 status)
+    assert moe.moe_get_device_status(status) == _abi.MOE_ERR_TIMEOUT
+    assert bool((out == 7).all())
+    _abi.moe_test_gemm_fp8_block(a, sa, w, sw, M, N, K, out, _abi.MOE_BF16, form)
+    _close(out, _dequant(a, sa), _dequant(w, sw, N), torch.bfloat16)
+
+
+def test_held_back_scales_need_a_wait_limit():
+    a, s = _codes((4, 128), 1), _scales((4, 1), 3)
+    out = torch.empty((4, 4), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoEError) as e:
+        _abi.moe_test_gemm_fp8_block(a, s, a, s[:1], 4, 4, 128, out, _abi.MOE_BF16, 16)
+    assert e.value.status == _abi.MOE_ERR_INVALID_ARG
