@@ -57,7 +57,10 @@ def _on(stream):
     if stream is None:
         return contextlib.nullcontext()
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+        # ExternalStream(0) would be a new stream of torch's pool; 1 is the
+        # runtime's other handle of the default stream
+        stream = (torch.cuda.default_stream() if stream in (0, 1)
+                  else torch.cuda.ExternalStream(stream))
     return torch.cuda.stream(stream)
 
 
