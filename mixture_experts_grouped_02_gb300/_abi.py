@@ -190,7 +190,7 @@ def status_string(status: int) -> str:
 
 
 def _p(t):
-    if t is None or type(t) is int:
+    if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")

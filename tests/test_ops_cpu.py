@@ -129,3 +129,12 @@ def test_tensors_of_other_devices_are_refused(call, monkeypatch):
         _device_calls(0, 1)[call]()
     with pytest.raises(ValueError, match="the current device is cuda:0"):
         _device_calls(1, 1)[call]()
+
+
+def test_pointers_of_an_int_subclass_are_taken():
+    """A handle type of the caller's own, as every entry point has taken."""
+    class Pointer(int):
+        pass
+
+    assert _abi._p(Pointer(A)) == A and _abi._p(A) == A and _abi._p(None) is None
+    assert _refused("moe_quantize_fp8_block", x=Pointer(A + 1)) == _abi.MOE_ERR_INVALID_ARG
