@@ -279,7 +279,10 @@ __global__ void __launch_bounds__(kThreads)
   const W* g = reinterpret_cast<const W*>(dout_) + static_cast<long long>(job / K) * row_words;
   const W* y = reinterpret_cast<const W*>(y_) + slot * row_words;
   dy += slot * row_words;
-  float dot = 0.0f;
+  // four chains to a lane, of H / 128 terms each: the error grows with a chain's
+  // length (T=4095 H=4096 K=2 fp32: 1.2e-7 relative, 2.1e-7 with one chain of
+  // H / 32; the time is the same, 88 us)
+  float dots[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int c0 = lane; c0 < row_words; c0 += 32 * U) {
     W gv[U], yv[U];
 #pragma unroll
@@ -296,12 +299,14 @@ __global__ void __launch_bounds__(kThreads)
         unpack<T, V>(yv[u], yf);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+          float& dot = dots[V == 1 ? u : i & 3];
           dot = fmaf(gf[i], yf[i], dot);
           gf[i] *= w;
         }
         dy[c0 + 32 * u] = pack<T, V>(gf);
       }
   }
+  float dot = (dots[0] + dots[1]) + (dots[2] + dots[3]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
   if (lane == 0) dw[job] = dot;
