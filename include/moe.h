@@ -506,8 +506,10 @@ int moe_unpermute_tokens_backward(const void* grad_out, const void* y, int dtype
  *   m = max(max |v|, 2^-100), scale[t, b] = m / 448,
  *   xq = e4m3_rn_satfinite(v * (448 / m)), in fp32 with IEEE rounding.
  * x (T, H) in x_dtype (MOE_BF16 or MOE_F32), v = x; with gated = 1, x (T, 2H)
- * holds gate then up and v = gate / (1 + e^-gate) * up in fp32 (fast exponential
- * and division).  xq (T, H) codes, scale (T, ceil(H/128)) fp32.  H as above.
+ * holds gate then up and v = gate / (1 + e^-gate) * up in fp32 with the fast
+ * exponential and division: v is within (8 + 1.2 |gate|) 2^-23 relative, and 0
+ * for gates below -87.3.  xq (T, H) codes, scale (T, ceil(H/128)) fp32.  H as
+ * above.
  * A NaN becomes a NaN code; a block with an infinity gets an infinite scale. */
 int moe_quantize_fp8_block(const void* x, int x_dtype, int T, int H, int gated, uint8_t* xq,
                            float* scale, void* stream);

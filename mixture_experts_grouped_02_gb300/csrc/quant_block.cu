@@ -33,6 +33,14 @@ constexpr int kThreads = 256;
 constexpr int kBlock = 128;
 constexpr float kAmaxFloor = 7.8886090522101181e-31f;  // 2^-100
 
+// SiLU by the fast exponential and division, as in the GEMMs' epilogues.  The
+// product is within 3e-7 of the 64-bit one for gates down to -16 (the same
+// formula in IEEE operations: 2.5e-7), 4e-6 at -80, where the exponent's
+// rounding grows with the gate, and 0 below -87.3, where SiLU is under 1e-36.
+// Of 33.6 million codes (T=16411 I=2048, normal gates) 37 miss the exact one
+// either way.  More exact forms cost the kernel its rate (T=16411 I=2048 bf16,
+// 26.7 us): the exponent's rounding made good 29.8 to 30.9, expf 31.4, expf of
+// -|g| 34.0, expf and an IEEE division 40.0.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }

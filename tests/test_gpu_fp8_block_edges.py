@@ -73,3 +73,23 @@ def test_held_back_scales_need_a_wait_limit():
     with pytest.raises(moe.MoEError) as e:
         _abi.moe_test_gemm_fp8_block(a, s, a, s[:1], 4, 4, 128, out, _abi.MOE_BF16, 16)
     assert e.value.status == _abi.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gated_precision_over_all_gates(dtype):
+    """The scale of a block of one value shows v itself.  The fast exponential
+    is within 2 + 1.173 |gate| units of the last place (2^-23), the fast division
+    within 2, three more operations and the scale's division are rounded once:
+    (8 + 1.2 |gate|) 2^-23."""
+    g = torch.cat([torch.linspace(-87, 87, 4001), torch.tensor([-87.25, -1e-3, 1e-30, 3e4])])
+    x = torch.zeros((g.numel(), 256))
+    x[:, 5], x[:, 133] = g, 2.0 ** 60
+    x = x.to(dtype)
+    q, s = moe.quantize_fp8_block(x.cuda(), gated=True)
+    gate = x[:, 5].double()
+    v = gate * torch.sigmoid(gate) * 2.0 ** 60
+    err = (s[:, 0].double().cpu() * 448 - v.abs()).abs()
+    seen = v.abs() > 2.0 ** -100
+    assert bool((err <= (8 + 1.2 * gate.abs()) * 2.0 ** -23 * v.abs())[seen].all())
+    assert int(seen.sum()) > 4000
+    assert bool((q[:, 5].cpu().double()[seen].abs() == 448).all())
