@@ -44,7 +44,8 @@ def _result(out, rows, N, dtype, device, stream):
 def quantize_fp8_block(x, gated=False, out=None, stream=None):
     """(codes (T, H) float8_e4m3fn, scales (T, ceil(H/128)) fp32) of x (T, H),
     or with gated of SiLU(gate) * up for x (T, 2H) holding gate then up.
-    out: a (codes, scales) pair to write instead."""
+    out: a (codes, scales) pair to write instead.  Every row is encoded: of a
+    sorted list the padding rows too, whatever they hold."""
     code = _dtype(x, _ROWS)
     T, H = x.shape
     if gated:
@@ -117,8 +118,9 @@ def forward_fp8_block(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, b
     per align block, by default 16 while the experts receive at most 16 rows
     on average and 128 above.  dev_status: an int32 status word of the
     caller's, zero at the start (one is made otherwise): an expert id out of
-    range is reported there, the later steps then do nothing and out is left
-    unspecified."""
+    range is reported there; permutation and products then do nothing and out is
+    not written, while the quantisers, which index nothing by the lists, encode
+    what their buffers hold."""
     from . import align
     T, H = x.shape
     if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or topk_ids.shape[0] != T:

@@ -93,3 +93,34 @@ def test_gated_precision_over_all_gates(dtype):
     assert bool((err <= (8 + 1.2 * gate.abs()) * 2.0 ** -23 * v.abs())[seen].all())
     assert int(seen.sum()) > 4000
     assert bool((q[:, 5].cpu().double()[seen].abs() == 448).all())
+
+
+@pytest.mark.parametrize("T,block_m", [(20, 16), (300, 128), (300, 256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_set_status_word_stops_the_grouped_product(T, block_m, dtype):
+    ids = torch.randint(0, 4, (T, 1), generator=_gen(1), device="cuda", dtype=torch.int32)
+    plan = moe.align(ids, 4, block_m)
+    cap = plan["sorted_ids"].numel()
+    out = torch.full((cap, 72), 7.0, dtype=dtype, device="cuda")
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    moe.grouped_gemm_fp8_block(_codes((cap, 128), 1), _scales((cap, 1), 2), _codes((4, 72, 128), 3),
+                               _scales((4, 1, 1), 4), plan, block_m, out=out, dev_status=status)
+    assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_an_id_out_of_range_leaves_the_layers_output(T):
+    """align reports it; no step that reads the lists then runs, and the
+    output keeps what it held."""
+    E, K, H, I = 4, 2, 256, 128
+    g = _gen(1)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    ids[T - 1, 1] = E
+    out = torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.forward_fp8_block(x, ids, torch.full((T, K), 0.5, device="cuda"),
+                          _codes((E, 2 * I, H), 3), _scales((E, 2, 2), 4), _codes((E, H, I), 5),
+                          _scales((E, 2, 1), 6), out=out, dev_status=status)
+    assert moe.moe_get_device_status(status) == _abi.MOE_ERR_DEVICE_BAD_ID
+    assert bool((out == 7).all())

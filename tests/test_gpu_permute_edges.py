@@ -26,3 +26,28 @@ def test_weight_gradient_of_one_large_term(H, dtype):
         _, dw = moe.unpermute_tokens_backward(g.cuda(), y.cuda(), plan, w.cuda())
         total = 2.0 ** 24 + H - 1
         assert float((dw.double() - total).abs().max()) <= p * 2.0 ** -24 * total
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [64, 61])
+def test_a_set_status_word_stops_every_step(dtype, H):
+    """Nothing is written, neither rows nor padding nor gradients."""
+    T, K = 8, 2
+    plan, slots, cap = _case(T, K, 4, 16)
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    x, y = torch.ones((T, H), dtype=dtype).cuda(), torch.ones((cap, H), dtype=dtype).cuda()
+    w = torch.ones((T, K), device="cuda")
+
+    def sevens(rows):
+        return torch.full((rows, H), 7.0, dtype=dtype, device="cuda")
+
+    for out in (moe.permute_tokens(x, plan, sevens(cap), status),
+                moe.permute_tokens_backward(y, plan, K, sevens(T), status),
+                moe.unpermute_tokens(y, plan, w, sevens(T), status),
+                moe.unpermute_tokens_backward(x, y, plan, w, sevens(cap), status)[0]):
+        assert bool((out == 7).all())
+    grad_w = torch.full((T, K), 7.0, device="cuda")
+    moe._abi.moe_unpermute_tokens_backward(x, y, moe.dtype_code(dtype), T, H, K, w,
+                                           plan["inv_perm"], plan["sorted_ids"], cap,
+                                           sevens(cap), grad_w, status)
+    assert bool((grad_w == 7).all())
