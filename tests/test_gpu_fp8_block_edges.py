@@ -124,3 +124,86 @@ def test_an_id_out_of_range_leaves_the_layers_output(T):
                           _scales((E, 2, 1), 6), out=out, dev_status=status)
     assert moe.moe_get_device_status(status) == _abi.MOE_ERR_DEVICE_BAD_ID
     assert bool((out == 7).all())
+
+
+def _gated_ref(x):
+    """(scales, values, block of each column) of gated rows in 64 bits."""
+    H = x.shape[1] // 2
+    v = x[:, :H].double() * torch.sigmoid(x[:, :H].double()) * x[:, H:].double()
+    p = torch.zeros((x.shape[0], _nblk(H) * 128), dtype=torch.float64, device=x.device)
+    p[:, :H] = v.abs()
+    return p.view(x.shape[0], -1, 128).amax(-1) / 448, v
+
+
+def _check_gated(x, q, s):
+    """The scale within (8 + 1.2 * 16 + 2) 2^-23 < 2^-18 of the exact one for
+    gates of at most 16; a code, half a step off, by 2^-4 of the value or half a
+    subnormal step, 2^-10 of the scale."""
+    sr, v = _gated_ref(x)
+    sd = s.double()
+    assert bool(((sd - sr).abs() <= 2.0 ** -18 * sr).all())
+    se = sd.repeat_interleave(128, 1)[:, :v.shape[1]]
+    err = (q.double() * se - v).abs()
+    assert bool((err <= (2.0 ** -4 + 2.0 ** -15) * v.abs() + 2.0 ** -10 * 1.001 * se).all())
+
+
+@pytest.mark.parametrize("T,H", [(3, 16), (1, 112), (7, 144), (50, 1008), (9, 128), (5000, 1040),
+                                 (16411, 2048), (9800, 272)])
+def test_gated_rows_of_words(T, H):
+    """bf16 rows of a multiple of 16 columns, which are walked by teams with the
+    next block's words in flight: one block to a team, several (from about 19,456
+    blocks on), and rows that end inside a block.  The magnitude changes by up to
+    2^30 from block to block, so a word of another block shows in the scale."""
+    g = _gen(T)
+    x = torch.randn(T, 2 * H, generator=g, device="cuda").clamp(-16, 16)
+    e = torch.randint(-15, 16, (T, _nblk(H)), generator=g, device="cuda").float()
+    x[:, H:] *= torch.exp2(2 * e).repeat_interleave(128, 1)[:, :H]
+    x = x.to(torch.bfloat16)
+    guard = torch.full((T + 2, H), 0x55, dtype=torch.uint8, device="cuda")
+    q, s = moe.quantize_fp8_block(x, gated=True, out=(
+        guard[1:-1], torch.full((T, _nblk(H)), float("nan"), device="cuda")))
+    for t0 in range(0, T, 2048):
+        r = slice(t0, t0 + 2048)
+        _check_gated(x[r], q[r].view(torch.float8_e4m3fn), s[r])
+    assert bool((guard[0] == 0x55).all()) and bool((guard[-1] == 0x55).all())
+
+
+@pytest.mark.parametrize("T,H,gated", [(300001, 7168, False), (150001, 7168, True)])
+def test_quantize_offsets_past_32_bits(T, H, gated):
+    """More than 2^31 elements: sampled rows are those of a call of their own,
+    which the other tests check, and of the formula."""
+    x = torch.randn(T, (2 if gated else 1) * H, device="cuda", dtype=torch.bfloat16).clamp_(-16, 16)
+    assert x.numel() > 2 ** 31
+    q, s = moe.quantize_fp8_block(x, gated=gated)
+    pick = torch.tensor([0, 1, T // 2, 2 ** 31 // x.shape[1] - 1, 2 ** 31 // x.shape[1],
+                         2 ** 31 // x.shape[1] + 1, T - 2, T - 1], device="cuda")
+    qp, sp = moe.quantize_fp8_block(x[pick], gated=gated)
+    qs = q.view(torch.uint8)[pick]
+    assert torch.equal(qs, qp.view(torch.uint8)) and torch.equal(s[pick], sp)
+    if gated:
+        _check_gated(x[pick], qp, sp)
+    else:
+        m = x[pick].double().abs().view(8, -1, 128).amax(-1)
+        assert bool(((sp.double() * 448 - m).abs() <= 2.0 ** -22 * m).all())
+
+
+@pytest.mark.parametrize("T,block_m", [(40, 16), (700, 128)])
+def test_gradient_of_the_grouped_products_rows(T, block_m):
+    """d a of sum(out * g): row s of expert e is g's row times w[e], the same
+    call on each expert's transposed codes and block scales."""
+    E, N, K = 4, 640, 400
+    ids = torch.randint(0, E, (T, 1), generator=_gen(3), device="cuda", dtype=torch.int32)
+    plan = moe.align(ids, E, block_m)
+    cap = plan["sorted_ids"].numel()
+    w, sw = _codes((E, N, K), 2), _scales((E, _nblk(N), _nblk(K)), 4)
+    gq, gs = moe.quantize_fp8_block(
+        torch.randn(cap, N, generator=_gen(7), device="cuda").to(torch.bfloat16))
+    wt = w.view(torch.uint8).transpose(1, 2).contiguous()
+    out = torch.full((cap, K), 777.0, dtype=torch.bfloat16, device="cuda")
+    moe.grouped_gemm_fp8_block(gq, gs, wt, sw.transpose(1, 2).contiguous(), plan, block_m, out=out)
+    seen = 0
+    for e, _, first, n in plan["block_info"][:int(plan["num_blocks"])].tolist():
+        r = slice(first, first + n)
+        _close(out[r], _dequant(gq[r], gs[r]), _dequant(w[e], sw[e], N).t(), torch.bfloat16)
+        seen += n
+    assert seen == T

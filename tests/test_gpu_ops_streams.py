@@ -56,3 +56,38 @@ def test_a_layer_on_the_default_streams_handle_waits_for_its_input(handle):
     late.zero_()
     rows = moe.permute_tokens(late, moe.align(ids, 8, 16, stream=handle), stream=handle)
     assert bool((rows == 0).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_a_layer_and_its_permutation_in_a_graph(T):
+    """Captured once and replayed on new inputs, as a caller does who cannot
+    spend the host's time on every call."""
+    E, K, H, I = 8, 2, 512, 256
+    x, ids, tw, weights = _layer(T, E, K, H, I)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    inputs = [(torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16),
+               torch.topk(torch.randn(T, E, generator=g, device="cuda"), K).indices.int())
+              for _ in range(3)]
+
+    def step():
+        out = moe.forward_fp8_block(x, ids, tw, *weights)
+        plan = moe.align(ids, E, 16)
+        rows = moe.permute_tokens(x, plan)
+        dx = moe.permute_tokens_backward(rows, plan, K)
+        y = moe.unpermute_tokens(rows, plan, tw)
+        dy, dw = moe.unpermute_tokens_backward(y, rows, plan, tw)
+        q, s = moe.quantize_fp8_block(x)
+        gemm = moe.gemm_fp8_block(q, s, weights[0][0], weights[1][0])
+        return out, rows, dx, y, dy, dw, q.view(torch.uint8), s, gemm
+
+    step()  # what is looked up once per device
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for nx, nids in inputs:
+        x.copy_(nx)
+        ids.copy_(nids)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
