@@ -36,7 +36,7 @@ constexpr int kWarps = kThreads / 32;
 // (the 120 padding rows of one token's list took 14 us as eight rows a warp,
 // 2 us so), and a long one up to a warp's worth, which keeps the CTAs few.
 int pad_slots(long long cap) {
-  return static_cast<int>(std::max(1ll, std::min(32ll, cap / (152 * 16))));
+  return static_cast<int>(std::max(1ll, std::min(32ll, cap / (device_sm_count() * 16))));
 }
 
 // A run of V elements of type T, loaded and stored as one word.

@@ -5,6 +5,11 @@ moe_unpermute_tokens and their ``_backward`` entry points.
 ``plan`` is the dict :func:`align` (or :func:`route_align`) returns; its
 ``inv_perm`` (T*K) and ``sorted_ids`` (cap) are read.  Rows are contiguous
 (rows, H) tensors; outputs are allocated when not given.
+
+Like every call of the package these compute on tensors and record nothing for
+autograd, also where an input requires a gradient: a training step calls the
+``_backward`` functions, or wraps both in a torch.autograd.Function as
+examples/fp8_expert_layer.py does.
 """
 from __future__ import annotations
 
