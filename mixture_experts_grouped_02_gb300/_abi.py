@@ -189,10 +189,15 @@ def status_string(status: int) -> str:
         return f"status {status}"
 
 
-def _p(t):
+def _p(t, device=None):
+    """Address of a contiguous CUDA tensor, on `device` if given."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda:
+    if device is not None:
+        if t.get_device() != device:
+            raise ValueError(f"expected a tensor on the current device cuda:{device}, got one on "
+                             f"{_where(t)}")
+    elif not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
@@ -205,10 +210,26 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream):
+def _where(t):
+    d = t.get_device()
+    return f"cuda:{d}" if d >= 0 else str(t.device)
+
+
+def _gpu(t):
+    """The current device, for the other tensors of a call to be checked
+    against: its kernels and stream are used, and another GPU's memory is no
+    valid address there.  None where t is none or a raw pointer."""
+    if t is None or isinstance(t, int):
+        return None
+    if t.get_device() < 0:
+        raise ValueError("expected a CUDA tensor")
+    return _device()
+
+
+def _stream(stream, device=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(_device())
+            return _raw_stream(_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -378,51 +399,63 @@ def moe_forward_noalloc_status(stream=None) -> int:
 
 def moe_permute_tokens(x, dtype, T, H, K, inv_perm, sorted_ids, cap, x_sorted, dev_status=None,
                        stream=None):
-    _check(lib().moe_permute_tokens(_p(x), dtype, T, H, K, _p(inv_perm), _p(sorted_ids), cap,
-                                    _p(x_sorted), _p(dev_status), _stream(stream)),
+    d = _gpu(x)
+    _check(lib().moe_permute_tokens(_p(x, d), dtype, T, H, K, _p(inv_perm, d), _p(sorted_ids, d),
+                                    cap, _p(x_sorted, d), _p(dev_status, d), _stream(stream, d)),
            "moe_permute_tokens")
 
 
 def moe_permute_tokens_backward(grad_sorted, dtype, T, H, K, inv_perm, cap, grad_x,
                                 dev_status=None, stream=None):
-    _check(lib().moe_permute_tokens_backward(_p(grad_sorted), dtype, T, H, K, _p(inv_perm), cap,
-                                             _p(grad_x), _p(dev_status), _stream(stream)),
+    d = _gpu(grad_sorted)
+    _check(lib().moe_permute_tokens_backward(_p(grad_sorted, d), dtype, T, H, K, _p(inv_perm, d),
+                                             cap, _p(grad_x, d), _p(dev_status, d),
+                                             _stream(stream, d)),
            "moe_permute_tokens_backward")
 
 
 def moe_unpermute_tokens(y, dtype, T, H, K, topk_weights, inv_perm, cap, out, dev_status=None,
                          stream=None):
-    _check(lib().moe_unpermute_tokens(_p(y), dtype, T, H, K, _p(topk_weights), _p(inv_perm), cap,
-                                      _p(out), _p(dev_status), _stream(stream)),
+    d = _gpu(y)
+    _check(lib().moe_unpermute_tokens(_p(y, d), dtype, T, H, K, _p(topk_weights, d),
+                                      _p(inv_perm, d), cap, _p(out, d), _p(dev_status, d),
+                                      _stream(stream, d)),
            "moe_unpermute_tokens")
 
 
 def moe_unpermute_tokens_backward(grad_out, y, dtype, T, H, K, topk_weights, inv_perm, sorted_ids,
                                   cap, grad_y, grad_weights, dev_status=None, stream=None):
-    _check(lib().moe_unpermute_tokens_backward(_p(grad_out), _p(y), dtype, T, H, K,
-                                               _p(topk_weights), _p(inv_perm), _p(sorted_ids),
-                                               cap, _p(grad_y), _p(grad_weights),
-                                               _p(dev_status), _stream(stream)),
+    d = _gpu(grad_out)
+    _check(lib().moe_unpermute_tokens_backward(_p(grad_out, d), _p(y, d), dtype, T, H, K,
+                                               _p(topk_weights, d), _p(inv_perm, d),
+                                               _p(sorted_ids, d), cap, _p(grad_y, d),
+                                               _p(grad_weights, d), _p(dev_status, d),
+                                               _stream(stream, d)),
            "moe_unpermute_tokens_backward")
 
 
 def moe_quantize_fp8_block(x, x_dtype, T, H, gated, xq, scale, stream=None):
-    _check(lib().moe_quantize_fp8_block(_p(x), x_dtype, T, H, int(gated), _p(xq), _p(scale),
-                                        _stream(stream)), "moe_quantize_fp8_block")
+    d = _gpu(x)
+    _check(lib().moe_quantize_fp8_block(_p(x, d), x_dtype, T, H, int(gated), _p(xq, d),
+                                        _p(scale, d), _stream(stream, d)),
+           "moe_quantize_fp8_block")
 
 
 def moe_gemm_fp8_block(a, a_scale, w, w_scale, M, N, K, out, out_dtype, dev_status=None,
                        stream=None):
-    _check(lib().moe_gemm_fp8_block(_p(a), _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out),
-                                    out_dtype, _p(dev_status), _stream(stream)),
+    d = _gpu(a)
+    _check(lib().moe_gemm_fp8_block(_p(a, d), _p(a_scale, d), _p(w, d), _p(w_scale, d), M, N, K,
+                                    _p(out, d), out_dtype, _p(dev_status, d), _stream(stream, d)),
            "moe_gemm_fp8_block")
 
 
 def moe_grouped_gemm_fp8_block(a, a_scale, w, w_scale, E, N, K, cap, block_m, block_info,
                                num_blocks, out, out_dtype, dev_status=None, stream=None):
-    _check(lib().moe_grouped_gemm_fp8_block(_p(a), _p(a_scale), _p(w), _p(w_scale), E, N, K, cap,
-                                            block_m, _p(block_info), _p(num_blocks), _p(out),
-                                            out_dtype, _p(dev_status), _stream(stream)),
+    d = _gpu(a)
+    _check(lib().moe_grouped_gemm_fp8_block(_p(a, d), _p(a_scale, d), _p(w, d), _p(w_scale, d), E,
+                                            N, K, cap, block_m, _p(block_info, d),
+                                            _p(num_blocks, d), _p(out, d), out_dtype,
+                                            _p(dev_status, d), _stream(stream, d)),
            "moe_grouped_gemm_fp8_block")
 
 

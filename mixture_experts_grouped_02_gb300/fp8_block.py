@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from .permute import (_dtype, _empty, _lists, _on, _on_current_device, _ROWS, permute_tokens,
+from .permute import (_dtype, _empty, _lists, _on, _ROWS, permute_tokens,
                       unpermute_tokens)
 
 
@@ -58,7 +58,6 @@ def quantize_fp8_block(x, gated=False, out=None, stream=None):
     else:
         _codes(out[0], (T, H), "out codes")
         _scales(out[1], (T, _nblk(H)), "out scales")
-    _on_current_device(x, out[0], out[1])
     _abi.moe_quantize_fp8_block(x, code, T, H, gated, out[0], out[1], stream)
     return out
 
@@ -73,7 +72,6 @@ def gemm_fp8_block(a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, d
     _scales(a_scale, (M, _nblk(K)), "a_scale")
     _scales(w_scale, (_nblk(N), _nblk(K)), "w_scale")
     out, code = _result(out, M, N, out_dtype, a.device, stream)
-    _on_current_device(a, a_scale, w, w_scale, out, dev_status)
     _abi.moe_gemm_fp8_block(a, a_scale, w, w_scale, M, N, K, out, code, dev_status, stream)
     return out
 
@@ -102,7 +100,6 @@ def grouped_gemm_fp8_block(a, a_scale, w, w_scale, plan, block_m=128, out=None,
     _scales(a_scale, (cap, _nblk(K)), "a_scale")
     _scales(w_scale, (E, _nblk(N), _nblk(K)), "w_scale")
     out, code = _result(out, rows, N, out_dtype, a.device, stream)
-    _on_current_device(a, a_scale, w, w_scale, info, num, out, dev_status)
     _abi.moe_grouped_gemm_fp8_block(a, a_scale, w, w_scale, E, N, K, cap, block_m, info, num, out,
                                     code, dev_status, stream)
     return out
@@ -131,13 +128,15 @@ def forward_fp8_block(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, b
     E = L if num_experts is None else num_experts
     if block_m is None:
         block_m = 16 if T * K <= 16 * E else 128
-    _on_current_device(x, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, out, dev_status)
     # every buffer below is made and used on the one stream
     with _on(stream):
         if out is None:
             out = torch.empty((T, H), dtype=x.dtype, device=x.device)
         if T == 0:
             return out
+        d = _abi._gpu(x)
+        for t in (topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, out, dev_status):
+            _abi._p(t, d)  # before the first step
         if dev_status is None:
             dev_status = torch.zeros(1, dtype=torch.int32, device=x.device)
         plan = align(topk_ids, E, block_m, dev_status, None, expert_base,

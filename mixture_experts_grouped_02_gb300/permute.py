@@ -44,18 +44,6 @@ def _rows(t, rows, H, dtype, what):
     return t
 
 
-def _on_current_device(*tensors):
-    """Raise unless the tensors (or None, or raw pointers) share the current
-    device: its kernels and its stream are used, and another GPU's memory is no
-    valid address there.  CPU tensors are refused at the call."""
-    first = tensors[0].get_device()
-    if first >= 0 and first != _abi._device():
-        raise ValueError(f"tensors on cuda:{first}, the current device is cuda:{_abi._device()}")
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.get_device() != first:
-            raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
-
-
 def _on(stream):
     """Context in which buffers for kernels on `stream` (None: the current
     one) are allocated, so that the allocator orders their reuse on it."""
@@ -105,7 +93,6 @@ def permute_tokens(x, plan, out=None, dev_status=None, stream=None):
     T, H = x.shape
     K = _topk(inv.numel(), T, "permute_tokens")
     out = _out(out, cap, H, x, "out", stream)
-    _on_current_device(x, inv, ids, out, dev_status)
     _abi.moe_permute_tokens(x, code, T, H, K, inv, ids, cap, out, dev_status, stream)
     return out
 
@@ -120,7 +107,6 @@ def permute_tokens_backward(grad_sorted, plan, K, out=None, dev_status=None, str
     T, H = inv.numel() // K, grad_sorted.shape[-1]
     _rows(grad_sorted, cap, H, grad_sorted.dtype, "grad_sorted")
     out = _out(out, T, H, grad_sorted, "out", stream)
-    _on_current_device(grad_sorted, inv, out, dev_status)
     _abi.moe_permute_tokens_backward(grad_sorted, code, T, H, K, inv, cap, out, dev_status, stream)
     return out
 
@@ -134,7 +120,6 @@ def unpermute_tokens(y, plan, topk_weights, out=None, dev_status=None, stream=No
     H = y.shape[-1]
     _rows(y, cap, H, y.dtype, "y")
     out = _out(out, T, H, y, "out", stream)
-    _on_current_device(y, inv, topk_weights, out, dev_status)
     _abi.moe_unpermute_tokens(y, code, T, H, K, topk_weights, inv, cap, out, dev_status, stream)
     return out
 
@@ -151,7 +136,6 @@ def unpermute_tokens_backward(grad_out, y, plan, topk_weights, out=None, dev_sta
     _rows(grad_out, T, H, y.dtype, "grad_out")
     out = _out(out, cap, H, y, "out", stream)
     grad_w = _empty((T, K), torch.float32, y.device, stream)
-    _on_current_device(y, grad_out, inv, ids, topk_weights, out, dev_status)
     _abi.moe_unpermute_tokens_backward(grad_out, y, code, T, H, K, topk_weights, inv, ids, cap,
                                        out, grad_w, dev_status, stream)
     return out, grad_w
