@@ -35,21 +35,22 @@
 //    4 and one half of the columns.  A warp whose 32 rows are all padding only
 //    keeps the barriers.
 //
-// 8192 x 4096 x 7168: 205 us at 1.85 GHz, 227 in a loop of seconds under the
-// power cap (2.35 and 2.12 PFLOP/s); 371,000 clocks, about 840 per stage of two
-// scale blocks inside a tile and 2500 more per tile for its output.  What
-// bounds a stage is shared memory: its MMAs need 512 clocks at the full rate and
+// 8192 x 4096 x 7168: 197 us in a burst of 12 launches, 219 in a loop of seconds
+// under the power cap (2.44 and 2.20 PFLOP/s; 1715 MHz, 375,000 clocks), about
+// 840 clocks per stage of two scale blocks inside a tile and 2500 more per tile
+// for its output.  What bounds a stage is shared memory: its MMAs need 512 clocks at the full rate and
 // take them when the operands stay in place (all SMs busy), reading 64 KB at
 // 128 bytes a clock; TMA's writes of the next 64 KB, at 256 bytes a clock, add
 // to that.  The sum, 768, is what a stage takes when the epilogue only hands the
 // buffers back (758; with 64 weight rows 576 and 560, with a quarter of A's
-// bytes 672 and 676).  Fewer bytes per product need wider tiles: sums of 256
-// columns do not fit the epilogue's registers (with 16 epilogue warps of 64
-// columns 1,030,000 clocks, as they spill), and CTA pairs (256 rows x 128
-// weight rows, cta_group::2) took 372,000 to 437,000 clocks with small changes
-// elsewhere in the kernel, at best 216 us under the cap: a buffer comes back
-// 1060 clocks after its last MMA there, and two buffers fill TMEM.  No gain
-// from: a second issuing thread (414,000), 16 epilogue warps (420,000), buffers
+// bytes 672 and 676).  Fewer bytes per product need wider tiles.  Tried: 256
+// columns with 16 epilogue warps, which spill at the 96 registers that so many
+// threads leave (1,030,000 clocks), and 256 rows x 128 weight rows on CTA pairs
+// (cta_group::2; 372,000 to 437,000 clocks with small changes elsewhere, at best
+// 216 us where this form took 227), whose buffers come back 1060 clocks after
+// their last MMA; pairs were left out as a second protocol for 5 %.  Not
+// tried: 256 columns with 8 epilogue warps of 128 sums on registers that the
+// other warps give up, and 256 x 256 pairs.  No gain from: a second issuing thread (414,000), 16 epilogue warps (420,000), buffers
 // given back by scale block (384,000), four buffers of 64 columns, L2 copies of
 // the weights ahead of the loads (393,000), outputs stored by TMA (384,000).
 //
@@ -839,9 +840,10 @@ Fp8bHeld fp8b_held() {
 
 // The form with the least estimated time: rounds of tiles times what a stage
 // takes (GB300, us: 0.36 with 64 weight rows, 0.55 with 128; 8192 x 4096 x 7168
-// took 268 and 204).  Measured around the choice: 333 x 2880 x 2880 in 8.1 us
-// with 64 rows and 9.8 with 128; 1024 x 4096 x 7168 in 43 and 33; 8192 rows of 32
-// experts against 4096 x 7168 in 407 and 296.  A sorted list's row blocks are
+// takes 274 and 219 under the power cap).  Measured around the choice, operands
+// from HBM: 333 x 2880 x 2880 in 8.6 us with 64 rows and 11.0 with 128; 1024 x
+// 4096 x 7168 in 41 and 32; 8192 rows of 32 experts against 4096 x 7168 in 407
+// and 296.  A sorted list's row blocks are
 // estimated from its capacity: at least one row per align block and all but
 // the padding of E blocks; half a block of padding per expert that has rows.
 Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
@@ -867,10 +869,10 @@ Fp8bForm fp8b_form(const Fp8bArgs& a, int sms, const Fp8bHeld& held) {
     f.grid = static_cast<int>(std::min<long long>(sms, max_blocks * n64));
     // Splitting K by s, where all the clusters are resident at once: 0.29 us
     // for every stage a CTA has less, against 2 us of cluster launch and
-    // barriers and 2.2 ns per row and partial sum to exchange them (16 x 576 x
-    // 7168: 11.2 us whole, 9.1, 7.4 and 6.7 by 2, 4 and 8; 128 x 576 x 7168:
-    // 11.7, 10.2, 8.8 and 9.1; 128 x 4096 x 7168: 13.1 whole, 11.5 by 2; 16 x
-    // 2880 x 2880: 6.8 whole, 7.2 by 2; 333 x 1024 x 4096: 8.8 and 9.0).
+    // barriers and 2.2 ns per row and partial sum to exchange them (operands from
+    // HBM, 16 x 576 x 7168: 11.9 us whole, 9.6, 7.8 and 7.0 by 2, 4 and 8; 128 x
+    // 576 x 7168: 12.7, 10.8, 9.3 and 9.7; 128 x 4096 x 7168: 13.8 whole, 12.7 by
+    // 2; 16 x 2880 x 2880: 7.6 whole, 7.9 by 2; 333 x 1024 x 4096: 8.9 and 9.2).
     const int stages = (a.k_tiles + 1) / 2;
     const double rows = a.block_info != nullptr ? std::min(a.block_m, 128) : std::min(a.M, 128);
     double best = 0.0;

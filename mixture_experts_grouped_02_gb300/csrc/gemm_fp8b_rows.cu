@@ -15,12 +15,16 @@
 // for every 2 KB of weights.  Row m of a fills column m of the MMA, so a NaN
 // or an infinite scale stays in its row.
 //
-// Bound by latency and, from a few thousand weight rows on, by HBM.  Measured
-// (us; the tcgen05 form in brackets): one row, 7168 x 2048 4.6 (7.0), 576 x
-// 7168 4.7 (6.5), 2048 x 7168 4.8 (8.0), 4096 x 7168 7.8 (11.4); eight rows,
-// 7168 x 2048 4.9 (6.4), 4096 x 7168 8.1 (10.8).  Sixteen rows, in two columns
-// of MMAs, gained 15 % at best and lost on others; lists of small blocks (16
-// rows, 64 blocks of N=4096 K=7168) took 143 against 119.
+// Bound by latency: a launch, and one trip to HBM per warp while 16 warps of
+// four blocks cover K, or two in turn with 8 warps to a CTA, as a warp's loads
+// wait in registers (four blocks, at the cap of 128 registers, where it spills 8
+// bytes).  Measured (us, weights from HBM; the best tcgen05 form in brackets):
+// one row, 7168 x 2048 5.9 (7.2), 576 x 7168 5.2 (6.7), 2048 x 7168 6.2 (8.8),
+// 4096 x 7168 9.6 (11.5), 45 % of the copy rate; eight rows, 7168 x 2048 6.2
+// (6.9), 4096 x 7168 10.3 (11.3).  With the weights in L2 one row takes 4.6 us for
+// 7168 x 2048 and 7.8 for 4096 x 7168.  Sixteen rows, in two columns of MMAs,
+// gained 15 % at best and lost on others; lists of small blocks (16 rows, 64
+// blocks of N=4096 K=7168) took 143 against 119.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -131,8 +135,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 }  // namespace
 
 // As many warps to a CTA as keep all CTAs resident at once (at 128 registers
-// an SM holds 16 warps), 4 at least: one row of 4096 x 7168 takes 7.8 us with 8
-// warps (256 CTAs) and 9.5 with 16, of 2048 x 7168 4.8 with 16 and 5.3 with 8.
+// an SM holds 16 warps), 4 at least: with the weights in L2 one row of 4096 x
+// 7168 takes 7.8 us with 8 warps (256 CTAs) and 9.5 with 16, of 2048 x 7168 4.8
+// with 16 and 5.3 with 8.
 cudaError_t launch_fp8b_rows(const Fp8bArgs& a, const uint8_t* x, const uint8_t* w, int sms,
                              cudaStream_t s) {
   const int ctas = (a.N + kRows - 1) / kRows;

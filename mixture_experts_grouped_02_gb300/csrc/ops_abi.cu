@@ -90,8 +90,8 @@ int run_gemm(Fp8bArgs a, const uint8_t* x, long long rows, const uint8_t* w, int
     return MOE_ERR_UNSUPPORTED;
   // Few rows: the kernel for them, as long as latency counts.  From 64 MB of
   // weights on both stream at HBM's rate and the tiles of the other one read a
-  // fewer times (us, 8 rows of 16384 x 7168: 28.6 and 23.7; 1 row of 16384 x
-  // 4096: 16.7 and 16.0; 8 rows of 4096 x 7168: 8.1 and 10.8).
+  // fewer times (us, 8 rows of 16384 x 7168: 28.4 and 23.4; 1 row of 16384 x
+  // 4096: 16.7 and 15.4; 8 rows of 4096 x 7168: 10.3 and 11.3).
   const bool few = a.block_info == nullptr && a.M <= kRowsMax &&
                    static_cast<long long>(a.N) * a.K <= (64ll << 20);
   if (force != nullptr ? force->bn == 16 : few)
