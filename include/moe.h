@@ -588,8 +588,9 @@ int moe_rms_norm_backward(const void* grad_out, const void* h, const void* weigh
  *   topk_weights (T, K) fp32 = scale * p[ids], divided by the sum of the K
  *   p[ids] with renormalize = 1 (0 where that sum is 0).
  * Equal choices and group scores go to the lower id.  Choices are compared
- * exactly to 2^-44 relative (scores below e^-86 of a row's largest, or of 1, count
- * as 0 where a bias or sums of two are compared).  E <= 1024, K <= 32.
+ * exactly to 2^-44 relative, sums of two to 2^-44 of their larger term (scores below
+ * e^-86 of a row's largest, or of 1, count as 0 where a bias or sums of two are
+ * compared).  E <= 1024, K <= 32.
  * A logit of -inf scores 0, also in a row of nothing else; a NaN is not
  * there (nor is a NaN choice).  Where fewer than K experts can be chosen, the
  * missing ones get id 0 and weight 0 and MOE_ERR_DEVICE_BAD_ID is recorded in

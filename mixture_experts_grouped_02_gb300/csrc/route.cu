@@ -473,22 +473,32 @@ __device__ __forceinline__ bool choose_fast(const RouteTokensArgs& a, const floa
       second = fmaxf(fmaxf(second, s2), fminf(s, s1));
       s = fmaxf(s, s1);
     }
-    if (a.top2 && a.run > 1) s += second;
+    // how far from the exact one a group's score may be: a sum's terms count, which may
+    // be far larger than the sum
+    float off = most + fabsf(s);
+    if (a.top2 && a.run > 1) {
+      off += fabsf(second);
+      s += second;
+    }
+    off *= kNear;
     // the group's first lane stands for it
     const int first = lane & ~(a.lanes - 1);
-    if (lane != first) s = -INFINITY;
+    const bool group = lane == first && h.n > 0;
+    float left = group ? s : -INFINITY;
     stays = false;
-    float last = 0.0f;
-    for (int k = 0; k <= a.topk_groups && k < a.groups; ++k) {
+    for (int k = 0; k < a.topk_groups; ++k) {
       int winner;
-      const float top = warp_top(s, winner);
-      if (k == a.topk_groups) {
-        if (BY_SCORE && !(last - top > 2.0f * kNear * (most + fabsf(last)))) return false;
-        break;
-      }
-      last = top;
-      if (lane == winner) s = -INFINITY;
+      warp_top(left, winner);
+      if (lane == winner) left = -INFINITY;
       stays |= first == winner;
+    }
+    if (BY_SCORE && a.topk_groups < a.groups) {
+      // every group that stays has to be clearly above every one that goes; a NaN of two
+      // infinities is not
+      const float low = group && stays ? fmaxf(s - off, -INFINITY) : INFINITY;
+      const float high = group && !stays ? fminf(s + off, INFINITY) : -INFINITY;
+      if (__reduce_min_sync(kFull, ordered(low)) <= __reduce_max_sync(kFull, ordered(high)))
+        return false;
     }
   }
   constexpr uint32_t kPlace = V - 1;
