@@ -630,8 +630,9 @@ int moe_route_tokens_backward(const float* grad_weights, const void* logits, int
  * MOE_ERR_UNSUPPORTED; any 1 <= N < 2^29 - 2048 and 0 <= M <= 2^31 - 513 (M == 0
  * does nothing); x and w 16-byte aligned.  fp32 outputs are sums of fp32 sums over
  * 512 elements each; bf16 ones of one fp32 accumulator over K, which the tensor
- * core leaves short of the exact sum by up to 1.2e-9 K relative.  Results do not
- * depend on the schedule.
+ * core leaves short of the exact sum by up to 1.2e-9 K relative, or, where K is over
+ * 65536, of sums over 32768 elements each, 4e-5 short.  Results do not depend on the
+ * schedule.
  *
  * Gradients, in three calls, of which a layer needs what it trains:
  * moe_linear_backward_act: grad_preact (M, N; SWIGLU: 2N) bf16 = grad_out * act'(z)
@@ -702,7 +703,7 @@ int moe_test_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uint8_
  * one CTA per tile of 64 and 128 weight rows, 2 to 4 the K range split over clusters
  * of 2, 4 and 8 CTAs, 5 the kernel for few rows (M <= 8, layout 0, no wait limit), 6 and
  * 7 CTA pairs per tile of 256 and 128 weight rows, 224 pairs per tile of as many (bf16
- * outputs).  wait_limit_ns as above; for tests. */
+ * outputs, K <= 65536).  wait_limit_ns as above; for tests. */
 int moe_test_linear(const void* x, const void* w, int M, int N, int K, int layout, int activation,
                     void* out, int out_dtype, int form, unsigned long long wait_limit_ns,
                     int32_t* dev_status, void* stream);

@@ -32,7 +32,9 @@
 // 2.1e-6 for K = 2048, 7.9e-6 for 7168).  That is nothing next to a bf16 output's
 // 2^-9, but fp32 outputs would lose 3 of their bits by it: for these
 // (LinearArgs::chunk) an accumulator sums 512 elements and the epilogue adds those
-// sums in fp32 registers.
+// sums in fp32 registers.  For bf16 outputs it sums all of K up to 65536 elements (7.2e-5,
+// a 27th of the output's rounding), beyond that 32768 at a time: a weight gradient over 2^20
+// rows would be 1.2e-3 short.
 //
 // SwiGLU: a tile's weight rows are BN / 2 gate rows and the up rows of the same
 // columns, and an epilogue warp has both halves of its columns.
@@ -67,6 +69,7 @@ constexpr int kStageOutBytes = kEpiWarps * 4096;  // 32 x 32 sums per epilogue w
 constexpr int kChunkRows = kBK;                   // M/N-major: a box of 64 columns x 64 K
 constexpr int kChunkBytes = kChunkRows * 128;
 constexpr int kPartPitch = 64 + 4;                // split: floats of a row of partial sums
+constexpr int kLongChunk = 32768 / kBK;           // K steps of an accumulator, bf16 and long K
 
 template <int BN_>
 struct Cfg {
@@ -836,6 +839,9 @@ cudaError_t prepare_pair() {
 
 int div_up(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
+// Whether a tile has one accumulator for all of K.
+bool one_accumulator(const LinearArgs& a) { return a.epi.out_bf16 && a.K <= kMostOfAccumulator; }
+
 template <int BN, bool SPLIT, bool AMN, bool BMN>
 cudaError_t launch_one(LinearArgs a, const LinearForm& f, const CUtensorMap& tmA,
                        const CUtensorMap& tmB, cudaStream_t s) {
@@ -864,8 +870,8 @@ cudaError_t launch_layout(const LinearArgs& a, const LinearForm& f, const CUtens
   if (f.pair && f.bn == 128)
     return launch_pair<128, true, AMN, BMN>(a, f, tmA, tmB, s);
   if (f.pair)
-    return a.epi.out_bf16 ? launch_pair<256, false, AMN, BMN>(a, f, tmA, tmB, s)
-                          : launch_pair<256, true, AMN, BMN>(a, f, tmA, tmB, s);
+    return one_accumulator(a) ? launch_pair<256, false, AMN, BMN>(a, f, tmA, tmB, s)
+                              : launch_pair<256, true, AMN, BMN>(a, f, tmA, tmB, s);
   if (f.splits > 1) return launch_one<64, true, AMN, BMN>(a, f, tmA, tmB, s);
   if (f.bn == 128) return launch_one<128, false, AMN, BMN>(a, f, tmA, tmB, s);
   return launch_one<64, false, AMN, BMN>(a, f, tmA, tmB, s);
@@ -930,7 +936,7 @@ LinearForm linear_form(const LinearArgs& a, int sms, const LinearHeld& held) {
   consider(128, true, 1, held.pairs, 0.182, 2.1, 6.0);
   consider(256, true, 1, held.pairs, 0.285, 3.0, 7.0);
   // the epilogue's first half of the warps has 128 columns of these too
-  if (a.epi.out_bf16) consider(224, true, 1, held.pairs, 0.272, 3.0, 7.0);
+  if (one_accumulator(a)) consider(224, true, 1, held.pairs, 0.272, 3.0, 7.0);
   for (int i = 0, s = 2; i < 3; ++i, s *= 2)
     consider(64, false, s, held.split[i], 0.16, 0.0, 5.8 + 0.3 * s);
   return best;
@@ -945,7 +951,9 @@ cudaError_t launch_linear(LinearArgs a, LinearLayout layout, const LinearForm& f
   a.bn = f.bn;
   a.band = std::min(a.n_tiles, f.bn > 128 ? 8 : 16);
   a.k_steps = div_up(a.K, kBK);
-  a.chunk = a.epi.out_bf16 ? a.k_steps + (a.k_steps & 1) : 512 / kBK;
+  a.chunk = !a.epi.out_bf16      ? 512 / kBK
+            : one_accumulator(a) ? a.k_steps + (a.k_steps & 1)
+                                 : kLongChunk;
   a.splits = f.splits;
   switch (layout) {
     case kRowsRows:

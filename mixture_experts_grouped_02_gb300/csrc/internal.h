@@ -378,6 +378,8 @@ struct LinearForm {
   bool pair;
   int splits, grid;
 };
+// Elements that one accumulator sums for a bf16 output at most (gemm_linear.cu).
+constexpr int kMostOfAccumulator = 65536;
 struct LinearHeld {
   int split[3];     // clusters of 2, 4 and 8 CTAs of the split form held at once
   int pairs;        // CTA pairs

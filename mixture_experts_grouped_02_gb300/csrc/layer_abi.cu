@@ -341,9 +341,10 @@ int moe_test_linear(const void* x, const void* w, int M, int N, int K, int layou
   f.bn = narrow ? 224 : kForms[form][0];
   f.pair = narrow || kForms[form][1] != 0;
   f.splits = narrow ? 1 : kForms[form][2];
-  // few rows: no waits and one layout; a split has K steps of 64 for all its CTAs
+  // few rows: no waits and one layout; a split has K steps of 64 for all its CTAs;
+  // 224 columns: one accumulator
   if ((f.bn == 16 && (M > kRowsMax || wait_limit_ns != 0 || layout != kRowsRows)) ||
-      (narrow && out_dtype != MOE_BF16) ||
+      (narrow && (out_dtype != MOE_BF16 || K > kMostOfAccumulator)) ||
       (K + 63) / 64 < f.splits)
     return MOE_ERR_UNSUPPORTED;
   LinearArgs a = linear_args(M, N, K, activation, out, out_dtype, dev_status);
