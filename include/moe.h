@@ -646,7 +646,8 @@ int moe_route_tokens_backward(const float* grad_weights, const void* logits, int
  *   multiples of 8, what is summed over (N here, M there) is at most 2^27, and
  *   grad_preact, w and x are 16-byte aligned.
  * moe_linear_backward_weight: grad_w (N, K) in out_dtype = grad_preact^T x, added to
- *   what grad_w holds with accumulate = 1.  M == 0 makes it zero, or leaves it. */
+ *   what grad_w holds with accumulate = 1.  M == 0 makes it zero, or leaves it.  N is
+ *   at most 2^30 - 4096 here. */
 typedef enum {
     MOE_LINEAR_NONE = 0,
     MOE_LINEAR_SILU = 1,

@@ -312,6 +312,7 @@ int moe_linear_backward_weight(const void* grad_preact, const void* x, int M, in
   // no rows: the sum is empty
   const int rc = check_linear(N, K, M == 0 ? 1 : M, MOE_LINEAR_NONE, out_dtype);
   if (rc != MOE_OK) return rc;
+  if (N > kMaxElements) return MOE_ERR_UNSUPPORTED;  // along the rows of grad_preact
   if (M == 0) {
     if (accumulate) return MOE_OK;
     if (!grad_w || !aligned(grad_w, elem_bytes(out_dtype))) return MOE_ERR_INVALID_ARG;
@@ -341,6 +342,7 @@ int moe_test_linear(const void* x, const void* w, int M, int N, int K, int layou
   f.bn = narrow ? 224 : kForms[form][0];
   f.pair = narrow || kForms[form][1] != 0;
   f.splits = narrow ? 1 : kForms[form][2];
+  if (layout == kColsCols && M > kMaxElements) return MOE_ERR_UNSUPPORTED;
   // few rows: no waits and one layout; a split has K steps of 64 for all its CTAs;
   // 224 columns: one accumulator
   if ((f.bn == 16 && (M > kRowsMax || wait_limit_ns != 0 || layout != kRowsRows)) ||

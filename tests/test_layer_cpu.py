@@ -256,3 +256,17 @@ def test_scratch_sizes_without_rows():
     assert _abi.moe_rms_norm_backward_scratch_bytes(0, 64) == 0
     assert _abi.moe_linear_backward_act_scratch_bytes(0, 64, 1) == 0
     assert _abi.moe_linear_backward_act_scratch_bytes(8, 64, 9) == 0
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_columns_of_grad_preact_past_what_tma_counts_are_refused(out_dtype, accumulate):
+    """They lie along the operand's rows, whose TMA coordinate is of 2 N bytes and the
+    tile's past them, in 32 bits."""
+    for n in (2 ** 30 - 4088, 2 ** 30, 2 ** 30 + 8, 2 ** 31 - 1024):
+        assert _refused("moe_linear_backward_weight", N=n, K=8, M=1, out_dtype=out_dtype,
+                        accumulate=accumulate) == UNSUPPORTED
+        for form in (0, 7):
+            with pytest.raises(moe.MoEError) as e:
+                _abi.moe_test_linear(A, A, n, 8, 8, 2, 0, A, out_dtype, form, 0, None, 0)
+            assert e.value.status == UNSUPPORTED
