@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(
     }
   }
   const float inv_h = 1.0f / static_cast<float>(a.H);
+  // h is multiplied by rstd before anything else: xhat is of ordinary size whatever h is
   for (int buf = 0; t < a.T; t += step, buf ^= 1) {
     const float rstd = a.rstd[t];
     const float2 rstd2 = make_float2(rstd, rstd);
@@ -693,15 +694,15 @@ __global__ void __launch_bounds__(
       if constexpr (WIDE) ring.get(t, 0, j, dy[j]), ring.get(t, 1, j, h[j]);
 #pragma unroll
       for (int i = 0; i < kVec / 2; ++i) {
-        const float2 p = __fmul2_rn(dy[j][i], h[j][i]);
-        dw2[j][i] = __ffma2_rn(p, rstd2, dw2[j][i]);
+        const float2 xhat = __fmul2_rn(h[j][i], rstd2);
+        const float2 p = __fmul2_rn(dy[j][i], xhat);
+        dw2[j][i] = __fadd2_rn(dw2[j][i], p);
         dot2 = __ffma2_rn(p, w[j][i], dot2);
+        if constexpr (!WIDE) h[j][i] = xhat;
       }
     }
-    // rstd times the mean of g * xhat, which rows of any magnitude keep in range
-    const float dot = team_sum<WARP_ROW ? 32 : 0>(dot2.x + dot2.y, s_sum[buf]);
-    const float k = rstd * (rstd * (dot * inv_h));
-    const float2 k2 = make_float2(-k, -k);
+    const float mean = team_sum<WARP_ROW ? 32 : 0>(dot2.x + dot2.y, s_sum[buf]) * inv_h;
+    const float2 mean2 = make_float2(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if constexpr (WIDE) {
@@ -712,8 +713,9 @@ __global__ void __launch_bounds__(
       float d[kVec];
 #pragma unroll
       for (int i = 0; i < kVec / 2; ++i) {
-        const float2 v =
-            __ffma2_rn(__ffma2_rn(h[j][i], k2, __fmul2_rn(dy[j][i], w[j][i])), rstd2, ds[j][i]);
+        const float2 xhat = WIDE ? __fmul2_rn(h[j][i], rstd2) : h[j][i];
+        const float2 v = __ffma2_rn(
+            __ffma2_rn(xhat, mean2, __fmul2_rn(dy[j][i], w[j][i])), rstd2, ds[j][i]);
         d[2 * i] = v.x;
         d[2 * i + 1] = v.y;
       }
