@@ -626,6 +626,7 @@ int moe_route_tokens_backward(const float* grad_weights, const void* logits, int
  *   and out = SiLU(z_gate) * z_up + residual.
  * SiLU by the fast exponential and division: within (8 + 1.2 |z|) 2^-23 relative,
  * 0 below -87.3; GELU within 2^-21 |z|, below 0 within (9 + z^2) 2^-23 relative.
+ * Both and their slopes take their limits at the infinities.
  * K a multiple of 8 (TMA rows start on 16 bytes) of at most 2^27, else
  * MOE_ERR_UNSUPPORTED; any 1 <= N < 2^29 - 2048 and 0 <= M <= 2^31 - 513 (M == 0
  * does nothing); x and w 16-byte aligned.  fp32 outputs are sums of fp32 sums over

@@ -47,7 +47,13 @@ __device__ __forceinline__ float2 gelu(float2 z) {
 __device__ __forceinline__ float2 sigmoid(float2 z) {
   return inverse_fast(__fadd2_rn(both(1.0f), exp2_fast(__fmul2_rn(z, both(-1.44269504f)))));
 }
-__device__ __forceinline__ float2 silu(float2 z) { return __fmul2_rn(z, sigmoid(z)); }
+// What an infinite z stands for beside a sigmoid of 0, or one less a sigmoid of 1: their product
+// is the limit 0 and no NaN.
+constexpr float kLargest = 3.402823466e38f;
+__device__ __forceinline__ float2 silu(float2 z, float2 s) {  // s = sigmoid(z)
+  return __fmul2_rn(make_float2(fmaxf(z.x, -kLargest), fmaxf(z.y, -kLargest)), s);
+}
+__device__ __forceinline__ float2 silu(float2 z) { return silu(z, sigmoid(z)); }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);

@@ -70,7 +70,12 @@ __device__ __forceinline__ void store8(__nv_bfloat16* row, int c, int n,
   }
 }
 
-// SiLU'(z) given s = sigmoid(z)
+// z within fp32's finite values
+__device__ __forceinline__ float2 finite(float2 z) {
+  return make_float2(fmaxf(fminf(z.x, kLargest), -kLargest),
+                     fmaxf(fminf(z.y, kLargest), -kLargest));
+}
+// SiLU'(z) given s = sigmoid(z); z finite
 __device__ __forceinline__ float2 silu_slope(float2 z, float2 s) {
   const float2 rest = __ffma2_rn(s, both(-1.0f), both(1.0f));
   return __fmul2_rn(s, __ffma2_rn(z, rest, both(1.0f)));
@@ -125,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(GATED))
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) {
             const float2 s = sigmoid(z[i]);
-            const float2 up = __fmul2_rn(d[i], __fmul2_rn(z[i], s));
-            d[i] = __fmul2_rn(__fmul2_rn(d[i], u[i]), silu_slope(z[i], s));
+            const float2 up = __fmul2_rn(d[i], silu(z[i], s));
+            d[i] = __fmul2_rn(__fmul2_rn(d[i], u[i]), silu_slope(finite(z[i]), s));
             u[i] = up;
             sum_up[i] = __fadd2_rn(sum_up[i], up);
           }
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(GATED))
         } else if (a.act == MOE_LINEAR_SILU) {
 #pragma unroll
           for (int i = 0; i < kPairs; ++i)
-            d[i] = __fmul2_rn(d[i], silu_slope(z[i], sigmoid(z[i])));
+            d[i] = __fmul2_rn(d[i], silu_slope(finite(z[i]), sigmoid(z[i])));
         } else if (a.act == MOE_LINEAR_GELU) {
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) d[i] = __fmul2_rn(d[i], gelu_slope(z[i]));

@@ -1,5 +1,6 @@
-"""The bf16 products over very long sums: against the formulas in 64 bits, with the
-bounds of test_gpu_linear.py unless a test derives its own."""
+"""The bf16 products over very long sums and at the ends of their activations:
+against the formulas in 64 bits, with the bounds of test_gpu_linear.py unless a test
+derives its own."""
 import pytest
 import torch
 
@@ -9,7 +10,7 @@ from test_gpu_linear import _act, _between, _rand
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
-NAN = float("nan")
+INF, NAN = float("inf"), float("nan")
 
 
 def _long(x, w):
@@ -69,3 +70,44 @@ def test_tiles_of_224_columns_have_one_accumulator():
     with pytest.raises(moe.MoEError) as e:
         _abi.moe_test_linear(x, w, 8, 8, 65544, 0, 0, out, _abi.MOE_BF16, 224)
     assert e.value.status == _abi.MOE_ERR_UNSUPPORTED
+
+
+# z, SiLU(z) and its slope there
+ENDS = [(INF, INF, 1.0), (-INF, 0.0, 0.0), (NAN, NAN, NAN), (1e38, 1e38, 1.0), (-1e38, 0.0, 0.0),
+        (-100.0, 0.0, 0.0), (0.0, 0.0, 0.5), (-0.0, 0.0, 0.5)]
+
+
+def _same(got, want):
+    want = torch.tensor(want, device="cuda").to(got.dtype).expand_as(got)
+    return torch.equal(got.nan_to_num(7.0, 3e38, -3e38), want.nan_to_num(7.0, 3e38, -3e38))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+@pytest.mark.parametrize("n", [8, 7])
+@pytest.mark.parametrize("M", [1, 300])
+def test_silu_at_the_ends(dtype, act, n, M):
+    """Infinities take the limits, inf and 0, in rows of words and of single elements."""
+    x = torch.ones((M, 8), dtype=BF16, device="cuda")
+    rows = 2 * n if act == "swiglu" else n
+    for z, y, _ in ENDS:
+        bias = torch.ones(rows, device="cuda")
+        bias[:n] = torch.tensor(z).to(BF16).float()
+        got = moe.linear(x, torch.zeros((rows, 8), dtype=BF16, device="cuda"), bias, act,
+                         out_dtype=dtype)
+        assert _same(got, torch.tensor(y).to(BF16).item()), z
+
+
+@pytest.mark.parametrize("n", [8, 7])
+def test_silus_slope_at_the_ends(n):
+    """1 and 0 at the infinities; SwiGLU's gradients have SiLU and its slope."""
+    for z, y, slope in ENDS:
+        pre = torch.full((1, n), z, device="cuda").to(BF16)
+        grad = torch.ones((1, n), dtype=BF16, device="cuda")
+        dz = torch.empty((1, n), dtype=BF16, device="cuda")
+        _abi.moe_linear_backward_act(grad, pre, 1, n, _abi.MOE_LINEAR_SILU, dz, None, None)
+        assert _same(dz, slope), z
+        both = torch.cat([pre, torch.full_like(pre, 2.0)], 1)
+        dz = torch.empty((1, 2 * n), dtype=BF16, device="cuda")
+        _abi.moe_linear_backward_act(grad, both, 1, n, _abi.MOE_LINEAR_SWIGLU, dz, None, None)
+        assert _same(dz[:, :n], 2 * slope) and _same(dz[:, n:], torch.tensor(y).to(BF16).item()), z
