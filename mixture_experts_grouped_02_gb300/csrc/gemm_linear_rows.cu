@@ -57,7 +57,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   __shared__ float s_part[kMaxWarps][kTokens][kRows];
   pdl_wait();
   pdl_launch_dependents();
-  if (p.status != nullptr && *reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  // One answer for the CTA, as the word may change while its warps start; it is needed when the
+  // sums are done and comes beside the weights.
+  __shared__ int s_stop;
+  int stop = 0;
+  if (threadIdx.x == 0 && p.status != nullptr)
+    stop = *reinterpret_cast<volatile int32_t*>(p.status);
   const bool gated = p.epi.act == MOE_LINEAR_SWIGLU;
   const int n0 = blockIdx.x * (gated ? kRows / 2 : kRows);  // the CTA's first output column
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -109,7 +114,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   s_part[warp][2 * t + 1][g] = acc[1];
   s_part[warp][2 * t][g + 8] = acc[2];
   s_part[warp][2 * t + 1][g + 8] = acc[3];
+  if (threadIdx.x == 0) s_stop = stop;
   __syncthreads();
+  if (s_stop != 0) return;
   __shared__ float s_sum[kTokens][kRows];
   for (int i = threadIdx.x; i < p.M * kRows; i += blockDim.x) {
     float v = 0.0f;

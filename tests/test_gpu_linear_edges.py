@@ -1,6 +1,6 @@
-"""The bf16 products over very long sums and at the ends of their activations:
-against the formulas in 64 bits, with the bounds of test_gpu_linear.py unless a test
-derives its own."""
+"""The bf16 products over very long sums, at the ends of their activations and
+beside a status word that is set while they start: against the formulas in 64 bits,
+with the bounds of test_gpu_linear.py unless a test derives its own."""
 import pytest
 import torch
 
@@ -111,3 +111,29 @@ def test_silus_slope_at_the_ends(n):
         dz = torch.empty((1, 2 * n), dtype=BF16, device="cuda")
         _abi.moe_linear_backward_act(grad, both, 1, n, _abi.MOE_LINEAR_SWIGLU, dz, None, None)
         assert _same(dz[:, :n], 2 * slope) and _same(dz[:, n:], torch.tensor(y).to(BF16).item()), z
+
+
+@pytest.mark.parametrize("M", [1, 8])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_a_status_word_that_is_set_meanwhile(M, act):
+    """From another stream, while the CTAs of the kernel for few rows start: each stores
+    its columns (16, SwiGLU: 8) whole and right, or leaves them alone."""
+    N, K, each = 8192, 512, 8 if act else 16
+    x, w = _rand((M, K), 1), _rand((2 * N if act else N, K), 2, scale=K ** -0.5)
+    want = moe.linear(x, w, activation=act)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for wait in range(0, 6000, 60):
+        status.zero_()
+        out = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        moe.linear(x, w, activation=act, out=out, dev_status=status)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(wait)
+            status.fill_(1)
+        torch.cuda.synchronize()
+        right, left = ((out == v).view(M, -1, each) for v in (want, 7.0))
+        # a CTA has its columns of every row
+        assert bool((right.all(2).all(0) | left.all(2).all(0)).all())
+    moe.linear(x, w, activation=act, out=out.fill_(7.0), dev_status=status)
+    assert bool((out == 7.0).all())
