@@ -17,7 +17,7 @@
 //
 // Bound by latency: a launch, and one trip to HBM per warp while 16 warps of
 // four blocks cover K, or two in turn with 8 warps to a CTA, as a warp's loads
-// wait in registers (four blocks, at the cap of 128 registers, where it spills 8
+// wait in registers (four blocks, at the cap of 128 registers, where it spills 16
 // bytes).  Measured (us, weights from HBM; the best tcgen05 form in brackets):
 // one row, 7168 x 2048 5.9 (7.2), 576 x 7168 5.2 (6.7), 2048 x 7168 6.2 (8.8),
 // 4096 x 7168 9.6 (11.5), 45 % of the copy rate; eight rows, 7168 x 2048 6.2
@@ -64,7 +64,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   __shared__ float s_part[kMaxWarps][kTokens][kRows];
   pdl_wait();
   pdl_launch_dependents();
-  if (p.status != nullptr && *reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  // One answer for the CTA, as the word may change while its warps start; it is needed when the
+  // sums are done and comes beside the weights.
+  __shared__ int s_stop;
+  int stop = 0;
+  if (threadIdx.x == 0 && p.status != nullptr)
+    stop = *reinterpret_cast<volatile int32_t*>(p.status);
   const int n0 = blockIdx.x * kRows;
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -118,7 +123,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   s_part[warp][2 * t + 1][g] = acc[1];
   s_part[warp][2 * t][g + 8] = acc[2];
   s_part[warp][2 * t + 1][g + 8] = acc[3];
+  if (threadIdx.x == 0) s_stop = stop;
   __syncthreads();
+  if (s_stop != 0) return;
   for (int i = threadIdx.x; i < p.M * kRows; i += blockDim.x) {
     const int m = i / kRows, c = i % kRows;
     if (n0 + c >= p.N) continue;

@@ -207,3 +207,29 @@ def test_gradient_of_the_grouped_products_rows(T, block_m):
         _close(out[r], _dequant(gq[r], gs[r]), _dequant(w[e], sw[e], N).t(), torch.bfloat16)
         seen += n
     assert seen == T
+
+
+@pytest.mark.parametrize("M", [1, 8])
+def test_a_status_word_that_is_set_meanwhile(M):
+    """From another stream, while the CTAs of the kernel for few rows start: each stores
+    its 16 columns whole and right, or leaves them alone."""
+    N, K = 8192, 512
+    a, w = _codes((M, K), 1), _codes((N, K), 2)
+    sa, sw = _scales((M, _nblk(K)), 3), _scales((_nblk(N), _nblk(K)), 4)
+    want = moe.gemm_fp8_block(a, sa, w, sw)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for wait in range(0, 6000, 60):
+        status.zero_()
+        out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        moe.gemm_fp8_block(a, sa, w, sw, out=out, dev_status=status)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(wait)
+            status.fill_(1)
+        torch.cuda.synchronize()
+        right, left = ((out == v).view(M, -1, 16) for v in (want, 7.0))
+        # a CTA has its columns of every row
+        assert bool((right.all(2).all(0) | left.all(2).all(0)).all())
+    moe.gemm_fp8_block(a, sa, w, sw, out=out.fill_(7.0), dev_status=status)
+    assert bool((out == 7.0).all())
