@@ -728,9 +728,11 @@ __global__ void __launch_bounds__(32 * kWarps)
 }  // namespace
 
 cudaError_t launch_route_tokens(RouteTokensArgs a, cudaStream_t s) {
-  // the smallest V for which every group has its lanes; where there is none (more than
-  // 4 groups of more than 128 experts) the experts lie through and groups are looked
-  // up one by one
+  // the smallest V for which every group has its lanes; where there is none (with G the
+  // next power of two from the groups' number on, more than 1024 / G experts to a group:
+  // 3 groups of more than 256, 5 of more than 128) the experts lie through, groups are
+  // looked up one by one, and every token is chosen by two-float scores (8192 tokens,
+  // 2 of 3 groups: of 256 experts 45 us, of 341 181)
   const int size = a.E / a.groups;
   int V = 1;
   a.by_lanes = 0;

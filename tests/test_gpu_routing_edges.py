@@ -40,3 +40,16 @@ def test_group_sums_that_cancel(most, size, where, scores):
         (left[:, :kept] - left[:, 1:kept + 1]).amin(1) > near)
     assert int(ok.sum()) > 0.9 * T
     _check(logits[ok], kept, scores, bias, groups, kept, "top2", True, 2.5)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups", [(1023, 3, 2), (771, 3, 1), (768, 3, 2),
+                                                  (640, 5, 3), (645, 5, 3), (576, 9, 4),
+                                                  (585, 9, 4), (544, 17, 5), (1020, 17, 5)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_on_both_sides_of_their_lanes(scores, E, groups, topk_groups, biased):
+    """Three groups of 256 experts have their own lanes of a warp, of 257 to 341 not; five
+    of 128, nine of 64 and seventeen of 32, but not of more."""
+    bias = _rand((E,), F32, 9, 0.1) if biased else None
+    for by in ("top2", "max"):
+        _check(_rand((37, E), F32, E, 2.0), 8, scores, bias, groups, topk_groups, by)
