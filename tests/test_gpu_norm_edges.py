@@ -1,19 +1,53 @@
-"""The RMS norm's gradients over values of any magnitude: against the formulas in 64
-bits, with the bounds of test_gpu_norm.py unless a test derives its own."""
+"""The RMS norm's gradients over many rows and over values of any magnitude:
+against the formulas in 64 bits, with the bounds of test_gpu_norm.py unless a test
+derives its own."""
 import pytest
 import torch
 
 import mixture_experts_grouped_02_gb300 as moe
+from mixture_experts_grouped_02_gb300 import _abi
 from test_gpu_norm import U, _grad_ref, _path, _rand
 
 pytestmark = pytest.mark.gpu
-F32 = torch.float32
+BF16, F32 = torch.bfloat16, torch.float32
 
 
 def _between(got, ref, d, dtype):
     assert got.dtype == dtype and got.shape == ref.shape
     bad = (got < (ref - d).to(dtype)) | (got > (ref + d).to(dtype)) | got.isnan()
     assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
+
+
+@pytest.mark.parametrize("H", [40, 257, 264, 1500, 1999, 2880, 2883, 4096, 8192])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("stream_grad", [False, True])
+def test_gradients_of_many_rows(H, dtype, stream_grad):
+    """Seven rows or more to every team that is resident, and a remainder: rows fetched
+    ahead at every depth, the slots gone round, and the weight gradient's terms
+    carried from row to row.  That takes fewer additions on a path than rows there are:
+    the team's rows, 8 in its CTA, the parts in 32 chains or more, 8 to join them."""
+    parts = _abi.moe_rms_norm_backward_scratch_bytes(1 << 20, H) // (4 * H)
+    teams = parts * (8 if H <= 512 else 1)
+    T = 7 * teams + 3
+    g = torch.Generator(device="cuda").manual_seed(H)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    dy, h = rand(T, H).to(dtype), rand(T, H).to(dtype)
+    ds = rand(T, H).to(dtype) if stream_grad else None
+    w = 1 + 0.2 * rand(H)
+    rstd = (h.double().square().mean(1) + 1e-6).rsqrt().float()
+    dx, dw = moe.rms_norm_backward(dy, h, w, rstd, ds)
+    ref, mag, terms = _grad_ref(dy, h, w, rstd, ds)
+    _between(dx, ref, (_path(H) + 10) * U * mag, dtype)
+    # CTAs may hold half as many rows at once in the other type or layout
+    path = 2 * 8 + 8 + parts / 32 + 1 + 8 + 4
+    _between(dw, terms.sum(0), path * U * terms.abs().sum(0), F32)
+    if ds is not None:
+        buf = ds.clone()
+        again = moe.rms_norm_backward(dy, h, w, rstd, buf, out=buf)
+        assert torch.equal(buf, dx) and torch.equal(again[1], dw)
 
 
 @pytest.mark.parametrize("H", [200, 1999, 2880, 8192, 9000])
