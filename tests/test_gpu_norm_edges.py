@@ -55,7 +55,7 @@ def test_gradients_of_values_of_any_magnitude(H):
     """Products of a row's values and their gradients that fp32 does not hold, or holds
     with few bits, of which the results have nothing."""
     for h_scale, dy_scale in ((1e25, 1e14), (1e-22, 1e-20), (1e30, 1e9), (1e-15, 1e-30),
-                              (1e-10, 1e25), (1e25, 1e-10)):
+                              (1e-10, 1e25), (1e25, 1e-10), (1e25, 1e-12)):
         h, dy = _rand((4, H), F32, 1, h_scale), _rand((4, H), F32, 2, dy_scale)
         w = _rand((H,), F32, 3)
         rstd = h.double().square().mean(1).rsqrt().float()
