@@ -544,6 +544,7 @@ int moe_grouped_gemm_fp8_block(const uint8_t* a, const float* a_scale, const uin
  * No counterpart on the pages: the step before the router and the experts.
  *   s = x + residual in fp32 (s = x without one), rstd = 1 / sqrt(mean(s^2) + eps),
  *   y = s * rstd * weight
+ * (in fp32: a row whose squares add up to more than 3.4e38 gets an rstd and a y of 0)
  * x, residual, sum and out (T, H) in dtype (MOE_BF16 or MOE_F32), weight (H) in
  * weight_dtype (either type), all of fp32 arithmetic with one rounding per output.
  * Outputs, each of which may be NULL, but not both out and codes:
@@ -619,8 +620,8 @@ int moe_route_tokens_backward(const float* grad_weights, const void* logits, int
  *   z = x w^T + bias,  out = act(z) + residual
  * in fp32, rounded once to out_dtype (MOE_BF16 or MOE_F32).
  *   x (M, K), w (N, K) bf16; bias (N) fp32 or NULL; residual (M, N) in out_dtype or
- *   NULL, may be out itself; preact (M, N) bf16 or NULL: z rounded, for the
- *   gradients; out (M, N).
+ *   NULL, may be out itself; preact (M, N) bf16 or NULL: z rounded, for the gradients;
+ *   out (M, N), which overlaps no other argument.
  *   MOE_LINEAR_SILU: z / (1 + e^-z), MOE_LINEAR_GELU: z (1 + erf(z / sqrt 2)) / 2,
  *   MOE_LINEAR_SWIGLU: w, bias and preact have 2N rows and columns, gate then up,
  *   and out = SiLU(z_gate) * z_up + residual.

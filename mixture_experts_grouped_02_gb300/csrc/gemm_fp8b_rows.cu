@@ -19,9 +19,9 @@
 // four blocks cover K, or two in turn with 8 warps to a CTA, as a warp's loads
 // wait in registers (four blocks, at the cap of 128 registers, where it spills 16
 // bytes).  Measured (us, weights from HBM; the best tcgen05 form in brackets):
-// one row, 7168 x 2048 5.9 (7.2), 576 x 7168 5.2 (6.7), 2048 x 7168 6.2 (8.8),
-// 4096 x 7168 9.6 (11.5), 45 % of the copy rate; eight rows, 7168 x 2048 6.2
-// (6.9), 4096 x 7168 10.3 (11.3).  With the weights in L2 one row takes 4.6 us for
+// one row, 7168 x 2048 5.9 (7.2), 576 x 7168 4.7 (6.7), 2048 x 7168 6.2 (8.8),
+// 4096 x 7168 9.2 (11.5), 47 % of the copy rate; eight rows, 7168 x 2048 6.2
+// (6.9), 4096 x 7168 10.0 (11.3).  With the weights in L2 one row takes 4.6 us for
 // 7168 x 2048 and 7.8 for 4096 x 7168.  Sixteen rows, in two columns of MMAs,
 // gained 15 % at best and lost on others; lists of small blocks (16 rows, 64
 // blocks of N=4096 K=7168) took 143 against 119.

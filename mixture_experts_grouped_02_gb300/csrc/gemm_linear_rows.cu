@@ -13,7 +13,7 @@
 // matter here.  Row m of x fills column m of the MMA, so a NaN stays in its row.
 //
 // Bound by HBM.  GB300, weights from HBM, us (at the copy rate of 6.8 TB/s): 1 x 4096 x
-// 7168 12.8 (8.6), 8 x 4096 x 7168 13.6 (8.7), 8 x 16384 x 7168 39 (34.6): a launch, one
+// 7168 12.5 (8.6), 8 x 4096 x 7168 13.3 (8.7), 8 x 16384 x 7168 39 (34.6): a launch, one
 // trip to HBM and the reduction are 3 to 4 us beside the streaming.  (The weights through
 // rings of shared memory: 12.8 and 58.)
 #include <cuda_bf16.h>

@@ -9,9 +9,12 @@
 // dz is rounded to bf16, the type of the operands of the products that follow;
 // the column sums are of the unrounded values: a thread adds eight columns of
 // every 8 x parts-th row, a CTA its eight row lanes, add_parts the CTAs, all in a fixed
-// order.  Bound by HBM: one read of dy and z, one write of dz.  GB300, operands from HBM, us
-// (at the copy rate of 6.8 TB/s): 4096 x 4096 SiLU 18.3 (14.8), with the bias's gradient 21.0,
-// GELU 20.8, SwiGLU of 2 x 2048 columns 16.6 (12.3), 8192 x 7168 SiLU 55.7 (51.8).
+// order.  One read of dy and z and one write of dz bound SiLU; GELU's arithmetic adds to them
+// (its kernel fills 56 % of the issue slots while its warps wait for HBM and for the arithmetic
+// pipes by turns), and the sums of the columns take a kernel of their own, 2.5 us.  GB300,
+// operands from HBM, us (at the copy rate of 6.8 TB/s): 4096 x 4096 SiLU 18.4 (14.8), with the
+// bias's gradient 20.7, GELU 21.5 and 23.8, SwiGLU of 2 x 2048 columns 16.5 and 19.3 (12.3),
+// 8192 x 7168 SiLU 56 (51.8).
 #include <cuda_bf16.h>
 
 #include <algorithm>

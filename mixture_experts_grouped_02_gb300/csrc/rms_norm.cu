@@ -20,7 +20,7 @@
 // the SM's teams then have on their way.  GB300, operands from HBM, us (copy rate 6.8
 // TB/s: us): T=8192 H=7168 bf16 rows 37.0 (34.5), with a residual and its sum 69.3 (69.1),
 // their codes as well 78.1 (77.7); fp32 rows 71.4 (69.1), with a residual 136 (138.2).
-// Gradients with the sum's: T=8192 H=4096 bf16 49.5 (39.5), H=7168 79 (69.1), fp32 149
+// Gradients with the sum's: T=8192 H=4096 bf16 49.3 (39.5), H=7168 79 (69.1), fp32 148
 // (138.2).
 #include <cuda_bf16.h>
 

@@ -27,10 +27,13 @@
 // whose unsigned order is the choices'; key 0 is below all of them and marks what
 // cannot be chosen.
 //
-// Bound by its instructions, some 800 a token where HBM would allow 100.  GB300, operands
-// from HBM, us (at the copy rate): 16384 tokens, top 8 of 256 experts, sigmoid, bias and 8
-// groups 19.8 (2.6), every token by two-float scores 46; softmax 12.6 (2.6), of 1024 experts
-// and 8192 tokens 23.4 (5.0); one token 2.9.
+// Bound by instructions and by what they wait for, not by HBM.  16384 tokens, top 8 of 256
+// experts, sigmoid, bias and 8 groups: 823 instructions a token where HBM would allow 100, which
+// fill two thirds of an SM's issue slots while it has warps and half of the kernel's time; the
+// rest are the rounds of the choice, each of which needs the one before it, and the first and
+// last warps.  GB300, operands from HBM, us (at the copy rate): 18.9 to 19.4 (2.6), every token
+// by two-float scores 46; softmax 12.6 to 12.9 (2.6; 647 instructions), of 1024 experts and 8192
+// tokens 23.4 (5.0); one token 3.0.
 //
 // Weights are fp32, from the logits by expf; renormalised ones relative to the
 // largest chosen, so that they do not underflow together.
