@@ -61,7 +61,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "bounds.cuh"
@@ -722,18 +721,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::kThreads, 1)
 
 template <int BN, int MODE>
 cudaError_t prepare_kernel() {
-  // once per device: the attribute outlives the launch
   static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(fp8b_gemm_kernel<BN, MODE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<BN, MODE>::kSmemBytes);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
+  return allow_smem(fp8b_gemm_kernel<BN, MODE>, Cfg<BN, MODE>::kSmemBytes, done);
 }
 
 template <int BN, int MODE>

@@ -44,7 +44,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "bounds.cuh"
@@ -812,29 +811,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- launches
 
-// A kernel's attribute, set once per device.
-template <typename K>
-cudaError_t prepare_kernel(K kern, int smem, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
-
 template <int BN, bool SPLIT, bool AMN, bool BMN>
 cudaError_t prepare_one() {
   static std::atomic<unsigned long long> done{0};
-  return prepare_kernel(linear_kernel<BN, SPLIT, AMN, BMN>, Cfg<BN>::kSmemBytes, done);
+  return allow_smem(linear_kernel<BN, SPLIT, AMN, BMN>, Cfg<BN>::kSmemBytes, done);
 }
 
 template <int PN, bool IN_REGS, bool AMN, bool BMN>
 cudaError_t prepare_pair() {
   static std::atomic<unsigned long long> done{0};
-  return prepare_kernel(linear_pair_kernel<PN, IN_REGS, AMN, BMN>, Cfg<PN / 2>::kSmemBytes, done);
+  return allow_smem(linear_pair_kernel<PN, IN_REGS, AMN, BMN>, Cfg<PN / 2>::kSmemBytes, done);
 }
 
 int div_up(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }

@@ -25,7 +25,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -394,20 +393,8 @@ struct Ring {
 
 int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
-// Shared memory above 48 KB has to be asked for; the most a launch may want, once per
-// device, so that calls at once do not take it from one another.
-template <typename K>
-cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done) {
-  constexpr int kMost = 226 * 1024;
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
+// The most shared memory that a gradient's launch may want.
+constexpr int kMostSmem = 226 * 1024;
 
 // How rows are dealt to CTAs: `threads` of a CTA, slots for `depth` rows, CTAs in all.
 struct RowForm {
@@ -872,7 +859,8 @@ template <typename T, bool WIDE, bool WARP_ROW, int VPT>
 cudaError_t launch_grad_rows(const RmsNormGradArgs& a, const GradForm& f, cudaStream_t s) {
   const size_t smem = f.rows.ring_bytes + (WARP_ROW ? warp_dw_bytes(a.H) : 0);
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t err = allow_smem(rms_norm_grad_kernel<T, WIDE, WARP_ROW, VPT>, done);
+  const cudaError_t err =
+      allow_smem(rms_norm_grad_kernel<T, WIDE, WARP_ROW, VPT>, kMostSmem, done);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg =
